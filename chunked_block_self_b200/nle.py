@@ -42,6 +42,16 @@ class PathBuffers(ctypes.Structure):
                                     "d_status")]
 
 
+class RopePlan(ctypes.Structure):
+    """nle_rope_plan."""
+    _fields_ = [(n, _vp) for n in ("cu_seqlens", "positions", "q_weight", "k_weight", "inv_freq", "dev_status")] + \
+        [("total_frames", _i64)] + [(n, _int) for n in ("n_seq", "q_heads", "k_heads", "d_head", "rot_dim",
+                                                        "interleaved")] + [("eps", _f32), ("rot_scale", _f32)]
+
+
+NLE_ROPE_BWD_WORKSPACE_BYTES = 1 << 20
+
+
 _SIGS = {
     "nle_version": ([], _int),
     "nle_path_fwd_host": ([ctypes.POINTER(PathBuffers), _int, _i64, _i64, _int, _int, _int, _int, _int, _int,
@@ -64,6 +74,8 @@ _SIGS = {
     "nle_varlen_attn_fwd": ([_vp, _vp, _vp, _vp, _vp, _int, _i64, _int, _int, _vp], _int),
     "nle_varlen_attn_fwd_ex": ([_vp, _vp, _vp, _vp, _vp, _int, _i64, _int, _int, _f32, _i64, _vp, _int, _i64,
                                 _vp], _int),
+    "nle_qk_norm_rope_fwd": ([ctypes.POINTER(RopePlan)] + [_vp, _i64] * 4 + [_vp], _int),
+    "nle_qk_norm_rope_bwd": ([ctypes.POINTER(RopePlan)] + [_vp, _i64] * 6 + [_vp] * 4, _int),
     "nle_ctc_greedy_fwd": ([_vp, _i64, _int, _vp, _int, _i64, _vp, _vp, _vp, _vp], _int),
     "nle_posterior_pool_fwd": ([_vp, _i64, _int, _vp, _i64, _int, _vp, _int, _i64, _int, _i64, _vp, _vp, _vp,
                                 _vp], _int),
@@ -120,6 +132,31 @@ def _dev_tensor(t, name, dtype):
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}")
+
+
+class _Scope:
+    """The device and stream that a call allocates and launches on: ``device``'s
+    current stream, or the one given.  What is allocated inside belongs to that
+    stream, so its memory cannot still be in use by work on another one."""
+
+    def __init__(self, device, stream):
+        self.ctx = None
+        if stream is not None:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(int(stream), device) if int(stream) else \
+                    torch.cuda.default_stream(device)
+            self.ctx = torch.cuda.stream(stream)
+        elif device.index != torch.cuda.current_device():
+            self.ctx = torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
 
 
 def nle_version() -> int:
@@ -262,6 +299,172 @@ def varlen_attn(q, k, v, cu_seqlens, out=None, stream=None) -> torch.Tensor:
         out = torch.empty_like(q)
     nle_varlen_attn_fwd(q, k, v, out, cu_seqlens, stream=stream)
     return out
+
+
+# ------------------------------------------------------------------ head norm + rotary positions
+def rope_inv_freq(rot_dim: int = 64, base: float = 10000.0, device="cuda", *, linear: float = 1.0,
+                  ntk: float = 1.0, yarn: float = 1.0, yarn_frames: int = 0, yarn_beta=(32.0, 1.0)):
+    """(inv_freq float64 [rot_dim / 2] on ``device``, rot_scale) of the rotary
+    rotation: inv_freq[j] = base ** (-2 j / rot_dim), stretched for contexts
+    longer than the trained ones by one of
+
+    * ``linear`` s: every frequency divided by s (position interpolation);
+    * ``ntk`` s: base * s ** (rot_dim / (rot_dim - 2)), which divides the
+      lowest frequency by s and leaves the highest;
+    * ``yarn`` s, with ``yarn_frames`` trained positions: frequencies that turn
+      more than ``yarn_beta[0]`` times over the trained positions stay, those
+      that turn fewer than ``yarn_beta[1]`` times are divided by s, a linear
+      ramp over the pair index between; rot_scale is 0.1 ln(s) + 1.
+    """
+    if rot_dim < 2 or rot_dim % 2 or not base > 1.0:
+        raise ValueError("rope_inv_freq: an even rot_dim >= 2 and a base above 1 are required")
+    if min(linear, ntk, yarn) < 1.0 or (linear > 1.0) + (ntk > 1.0) + (yarn > 1.0) > 1:
+        raise ValueError("rope_inv_freq: at most one of linear, ntk and yarn, each at least 1")
+    j = np.arange(rot_dim // 2, dtype=np.float64)
+    if ntk > 1.0 and rot_dim > 2:
+        base = base * ntk ** (rot_dim / (rot_dim - 2))
+    f = base ** (-2.0 * j / rot_dim)
+    scale = 1.0
+    if linear > 1.0:
+        f = f / linear
+    if yarn > 1.0:
+        if yarn_frames < 1 or not yarn_beta[0] > yarn_beta[1] > 0:
+            raise ValueError("rope_inv_freq: yarn needs yarn_frames >= 1 and yarn_beta (fast, slow), fast > slow > 0")
+        # pair index whose frequency turns n times over yarn_frames positions
+        fast, slow = (rot_dim * np.log(yarn_frames / (n * 2.0 * np.pi)) / (2.0 * np.log(base)) for n in yarn_beta)
+        lo, hi = max(np.floor(fast), 0.0), min(np.ceil(slow), rot_dim - 1.0)
+        keep = 1.0 - np.clip((j - lo) / max(hi - lo, 1e-3), 0.0, 1.0)
+        f = f * keep + f / yarn * (1.0 - keep)
+        scale = float(0.1 * np.log(yarn) + 1.0)
+    return torch.from_numpy(f).to(device), scale
+
+
+def _rows(t, name: str, frames: int | None = None, device=None):
+    """Checks a bf16 [frames, heads, 64] CUDA tensor whose heads are dense
+    (frames may be strided); returns its row stride."""
+    _dev_tensor(t, name, torch.bfloat16)
+    if t.dim() != 3 or t.shape[2] != 64:
+        raise ValueError(f"{name}: [frames, heads, 64] required")
+    if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != 64)):
+        raise ValueError(f"{name}: dense heads of 64 required (only the frame stride may vary)")
+    if frames is not None and t.shape[0] != frames:
+        raise ValueError(f"{name}: {frames} frames required")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name}: on {t.device}, the other tensors on {device}")
+    return t.stride(0) if t.shape[0] > 1 else 0
+
+
+def _on(device, **tensors):
+    """Every given tensor lies on ``device``."""
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name}: on {t.device}, the other tensors on {device}")
+
+
+def _rope_plan(ref, q_heads, k_heads, cu_seqlens, inv_freq, q_weight, k_weight, eps, interleaved, rot_scale, positions,
+               dev_status):
+    """nle_rope_plan of checked tensors; ``ref``: a [frames, heads, 64] tensor."""
+    frames, dev = ref.shape[0], ref.device
+    if cu_seqlens is None and positions is None:
+        raise ValueError("cu_seqlens or positions is required")
+    for t, n, dt in ((cu_seqlens, "cu_seqlens", torch.int32), (positions, "positions", torch.int32),
+                     (q_weight, "q_weight", torch.bfloat16), (k_weight, "k_weight", torch.bfloat16),
+                     (inv_freq, "inv_freq", torch.float64), (dev_status, "dev_status", torch.int32)):
+        if t is not None:
+            _dev_tensor(t, n, dt)
+            if not t.is_contiguous():
+                raise ValueError(f"{n}: contiguous tensor required")
+    _on(dev, cu_seqlens=cu_seqlens, positions=positions, q_weight=q_weight, k_weight=k_weight, inv_freq=inv_freq,
+        dev_status=dev_status)
+    if cu_seqlens is not None and cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens: [n_seq + 1] required")
+    if positions is not None and positions.numel() != frames:
+        raise ValueError(f"positions: [{frames}] required")
+    for t, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if t is not None and t.numel() != 64:
+            raise ValueError(f"{n}: [64] required")
+    rot_dim = 0 if inv_freq is None else 2 * inv_freq.numel()
+    return RopePlan(_ptr(cu_seqlens), _ptr(positions), _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq),
+                    _ptr(dev_status), frames, 0 if cu_seqlens is None else cu_seqlens.numel() - 1, q_heads, k_heads, 64,
+                    rot_dim, int(interleaved), float(eps), float(rot_scale))
+
+
+def _outputs(out, like, names, strides):
+    """The tensors to write: those of ``out``, checked, or new dense ones; their
+    row strides are appended to ``strides``."""
+    if out is None:
+        strides += [0] * len(like)
+        return [None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in like]
+    if len(out) != len(like):
+        raise ValueError(f"out: {', '.join(names)} required")
+    for o, t, n in zip(out, like, names):
+        if t is None:
+            strides.append(0)
+            continue
+        strides.append(_rows(o, n, t.shape[0], t.device))
+        if o.shape != t.shape:
+            raise ValueError(f"{n}: shape {tuple(t.shape)} required")
+    return out
+
+
+def qk_norm_rope(q, k, cu_seqlens, inv_freq, q_weight=None, k_weight=None, eps: float = 1e-6,
+                 interleaved: bool = False, rot_scale: float = 1.0, positions=None, out=None, dev_status=None,
+                 stream=None):
+    """(q_out, k_out): per-head RMS norm (with weights) and rotary rotation of
+    q [frames, q_heads, 64] and k [frames, k_heads, 64] (either may be None).
+    ``inv_freq``: float64 from :func:`rope_inv_freq` (None: no rotation).
+    ``out``: (q_out, k_out) to write, which may be (q, k); frames of no
+    utterance are not written."""
+    ref = q if q is not None else k
+    if ref is None:
+        raise ValueError("q or k is required")
+    strides = []
+    for t, n in ((q, "q"), (k, "k")):
+        strides.append(0 if t is None else _rows(t, n, ref.shape[0], ref.device))
+    plan = _rope_plan(ref, 0 if q is None else q.shape[1], 0 if k is None else k.shape[1], cu_seqlens, inv_freq,
+                      q_weight, k_weight, eps, interleaved, rot_scale, positions, dev_status)
+    with _Scope(ref.device, stream) as sid:
+        q_out, k_out = _outputs(out, (q, k), ("q_out", "k_out"), strides)
+        _check(_lib.nle_qk_norm_rope_fwd(ctypes.byref(plan), _ptr(q), strides[0], _ptr(k), strides[1], _ptr(q_out),
+                                         strides[2], _ptr(k_out), strides[3], sid), "nle_qk_norm_rope_fwd")
+    return q_out, k_out
+
+
+def qk_norm_rope_bwd(dq_out, dk_out, cu_seqlens, inv_freq, q=None, k=None, q_weight=None, k_weight=None,
+                     eps: float = 1e-6, interleaved: bool = False, rot_scale: float = 1.0, positions=None, out=None,
+                     dev_status=None, stream=None):
+    """(dq, dk, dq_weight, dk_weight) of :func:`qk_norm_rope` from the
+    gradients of its outputs (either may be None) and, with weights, its
+    inputs q and k.  The weights' gradients are float32 [64] (None without
+    weights).  ``out``: (dq, dk) to write, which may be (dq_out, dk_out)."""
+    ref = dq_out if dq_out is not None else dk_out
+    if ref is None:
+        raise ValueError("dq_out or dk_out is required")
+    norm = q_weight is not None or k_weight is not None
+    strides, x_strides = [], []
+    for d, x, w, n in ((dq_out, q, q_weight, "q"), (dk_out, k, k_weight, "k")):
+        strides.append(0 if d is None else _rows(d, f"d{n}_out", ref.shape[0], ref.device))
+        x_strides.append(0)
+        if d is not None and norm:
+            if x is None or w is None:
+                raise ValueError(f"{n} and {n}_weight are required for the gradient of the norm")
+            x_strides[-1] = _rows(x, n, ref.shape[0], ref.device)
+            if x.shape != d.shape:
+                raise ValueError(f"d{n}_out and {n}: one shape required")
+    plan = _rope_plan(ref, 0 if dq_out is None else dq_out.shape[1], 0 if dk_out is None else dk_out.shape[1],
+                      cu_seqlens, inv_freq, q_weight, k_weight, eps, interleaved, rot_scale, positions, dev_status)
+    with _Scope(ref.device, stream) as sid:
+        dq, dk = _outputs(out, (dq_out, dk_out), ("dq", "dk"), strides)
+        dw_q = dw_k = work = None
+        if norm:
+            dw_q = None if dq_out is None else torch.empty(64, dtype=torch.float32, device=ref.device)
+            dw_k = None if dk_out is None else torch.empty(64, dtype=torch.float32, device=ref.device)
+            work = torch.empty(NLE_ROPE_BWD_WORKSPACE_BYTES, dtype=torch.uint8, device=ref.device)
+        _check(_lib.nle_qk_norm_rope_bwd(ctypes.byref(plan), _ptr(dq_out), strides[0], _ptr(dk_out), strides[1],
+                                         _ptr(q) if norm else None, x_strides[0], _ptr(k) if norm else None,
+                                         x_strides[1], _ptr(dq), strides[2], _ptr(dk), strides[3], _ptr(dw_q),
+                                         _ptr(dw_k), _ptr(work), sid), "nle_qk_norm_rope_bwd")
+    return dq, dk, dw_q, dw_k
 
 
 # ------------------------------------------------------------------ windowed cross-attention

@@ -228,6 +228,75 @@ int nle_varlen_attn_fwd_ex(const void *q, const void *k, const void *v, void *ou
                            int64_t wait_limit_ns, void *stream);
 
 /* ---------------------------------------------------------------------
+ * Per-head RMS norm of queries and keys and the rotary position rotation, in
+ * one pass, and the gradient (the positions of the bidirectional editor's
+ * attention; the rotated q and k are what nle_varlen_attn_fwd takes).
+ * For every frame and head, with x the head's 64 values:
+ *     z = w * x / sqrt(mean(x^2) + eps)          (z = x without weights)
+ *     y_a = c (z_a cos t - z_b sin t),  y_b = c (z_b cos t + z_a sin t)
+ * for each pair (a, b): (j, j + rot_dim/2), or (2j, 2j + 1) when
+ * interleaved, j = 0 .. rot_dim/2 - 1, with t = position * inv_freq[j] and
+ * c = rot_scale; elements rot_dim .. 63 of z pass through.  Angles are formed
+ * in fp64, values in fp32, outputs rounded once to bf16.
+ *
+ * nle_rope_plan (host struct, pointers to device memory):
+ *   cu_seqlens   int32 [n_seq + 1], or NULL with n_seq ignored: every frame
+ *                of [0, total_frames), positions required.  Frames of no
+ *                utterance are neither read nor written; invalid utterances
+ *                are skipped and reported to dev_status
+ *   positions    nullable int32 [total_frames]; NULL: a frame's index inside
+ *                its utterance
+ *   total_frames rows of every tensor, at most 2^31 - 1
+ *   q_heads, k_heads  either may be 0 (that tensor's pointers are ignored)
+ *   d_head       must be 64
+ *   q_weight, k_weight  bf16 [64], 16-byte aligned; both NULL: no norm
+ *   eps          >= 0
+ *   inv_freq     double [rot_dim / 2] (may be NULL when rot_dim is 0)
+ *   rot_dim      0, 16, 32, 48 or 64
+ *   interleaved  0 or 1
+ *   rot_scale    0 selects 1
+ *   dev_status   nullable int32: receives NLE_ERR_INVALID_ARG
+ * Tensors are bf16 [total_frames][heads][64], 16-byte aligned; each *_stride
+ * is the elements between its frames (0: heads * 64; a multiple of 8, at
+ * least heads * 64), so that they may lie inside a fused projection buffer.
+ *
+ * nle_qk_norm_rope_fwd: q_out, k_out from q, k.  An output may be its input
+ * (same pointer and stride); other overlaps are not allowed.
+ * nle_qk_norm_rope_bwd: from the gradients dq_out, dk_out of the outputs and
+ * (read only with weights; may be NULL without) the inputs q, k: dq, dk, and
+ * the weights' gradients dq_weight, dk_weight: nullable float [64], written,
+ * not accumulated.  dq may be dq_out and dk dk_out.  workspace: with weights,
+ * NLE_ROPE_BWD_WORKSPACE_BYTES of device scratch, 16-byte aligned, used by
+ * this call alone until it has run; its content need not be kept.  Results
+ * are the same bits on every call.
+ * One kernel on `stream` (two for the weights' gradients); no allocation.
+ * Errors as for the attention entry points, before any launch.
+ */
+#define NLE_ROPE_BWD_WORKSPACE_BYTES (1 << 20)
+
+typedef struct {
+    const int32_t *cu_seqlens;
+    const int32_t *positions;
+    const void *q_weight, *k_weight;
+    const double *inv_freq;
+    int32_t *dev_status;
+    int64_t total_frames;
+    int n_seq, q_heads, k_heads, d_head;
+    int rot_dim, interleaved;
+    float eps, rot_scale;
+} nle_rope_plan;
+
+int nle_qk_norm_rope_fwd(const nle_rope_plan *plan, const void *q, int64_t q_stride, const void *k,
+                         int64_t k_stride, void *q_out, int64_t q_out_stride, void *k_out,
+                         int64_t k_out_stride, void *stream);
+
+int nle_qk_norm_rope_bwd(const nle_rope_plan *plan, const void *dq_out, int64_t dq_out_stride,
+                         const void *dk_out, int64_t dk_out_stride, const void *q, int64_t q_stride,
+                         const void *k, int64_t k_stride, void *dq, int64_t dq_stride, void *dk,
+                         int64_t dk_stride, float *dq_weight, float *dk_weight, void *workspace,
+                         void *stream);
+
+/* ---------------------------------------------------------------------
  * CTC greedy decoding of the encoder's CTC head (q4-RTN ONNX page,
  * "Inference note (NAR decode)"): the head emits n_classes per frame with
  * the blank at class 0, and a non-blank class c is token c - 1.  Per frame
