@@ -1,0 +1,842 @@
+// attn_bwd_sm100a.cu -- gradient of block attention and of full-utterance
+// attention on B200 (sm_100a), the probabilities recomputed from the
+// forward's log-sum-exp.
+//
+// For every segment (a block of an utterance, or the whole utterance) and
+// head, with s = softmax_scale, all sums over the segment's frames:
+//     P_ij  = exp(s q_i.k_j - lse_i)        delta_i = sum_d dO_id O_id
+//     dS_ij = P_ij (dO_i.v_j - delta_i)
+//     dV_j  = sum_i P_ij dO_i     dQ_i = s sum_j dS_ij k_j
+//     dK_j  = s sum_i dS_ij q_i
+//
+// Two kinds of work item, each owning 128 rows of one head and walking the
+// segment's other side in tiles of 128, so that every sum stays in the
+// owner's TMEM accumulators: no atomics, no partial sums in memory, the same
+// bits every time.  With X, Y the owner's and x, y the tile's matrices:
+//   kind 0 (dK, dV): owner K, V (rows = keys), tiles Q, dO
+//     S = X x^T, D = Y y^T (both transposed: row = key, column = query),
+//     acc0 (dK) += dS x,  acc1 (dV) += P y
+//   kind 1 (dQ): owner Q, dO (rows = queries), tiles K, V
+//     S = X x^T, D = Y y^T,  acc0 (dQ) += dS x
+// P is formed twice (once per kind): 7 products of 2*64 FLOP and 2 exps per
+// (query, key) pair instead of 5 and 1, which costs less than the fp32
+// atomics (32 KB per 128 x 128 tile) that a single pass would add.
+//
+// One persistent CTA per SM, 12 warps:
+//   warp 0   TMA producer: owner tiles (two stages), the segment's tiles into
+//            a ring; publishes every item's descriptor.
+//   warp 1   MMA issuer (one elected lane).  S and D of tile t + 1 are issued
+//            before the accumulating MMAs of tile t, so they run while the
+//            elementwise warps work on tile t.
+//   warp 2   tile fix-up: zeroes tile rows past the segment (up to the MMA's
+//            16-row granule: their P is 0, but 0 * Inf would be NaN) and, for
+//            kind 0, stages the tile's lse and delta (+inf and 0 past the
+//            segment, so that P and dS vanish there).
+//   warp 3   owns TMEM.
+//   warps 4-11  elementwise, two warpgroups: every lane owns one row of the
+//            tile (its TMEM lane), warpgroup g the columns 64g..64g+63:
+//            P = exp2(S s log2e - lse log2e), dS = P (D - delta) in fp32, both
+//            rounded once to bf16 (the A operands of the accumulating MMAs)
+//            and written over S; then the output rows (acc times s, rounded
+//            to bf16, 16-byte stores of the segment's rows only).
+// TMEM (512 columns): S buffers at 0 and 128 (after use: warpgroup g's P in
+// columns 64g..64g+31, its dS in 64g+32..64g+63), D at 256, acc0 at 384,
+// acc1 at 448.
+//
+// Every mbarrier wait is bounded; on expiry the CTA drains its copies and
+// MMAs in flight, frees TMEM and returns.
+#include <cmath>
+
+#include "nle.h"
+#include "nle_device.cuh"
+#include "nle_host.h"
+
+namespace {
+
+using namespace nle;
+
+constexpr int kThreads = 384;
+constexpr int kElem0 = 4;                            // first elementwise warp
+constexpr int kElemWarps = 8;
+constexpr int kRows = 128;                           // owner rows, and rows of a tile
+constexpr int kRowBytes = 128;                       // one frame of one head: 64 bf16
+constexpr uint32_t kMatBytes = kRows * kRowBytes;    // 16 KB
+constexpr uint32_t kPairBytes = 2 * kMatBytes;       // X, Y (owner) or x, y (tile)
+constexpr uint32_t kColBytes = 2 * kRows * 4;        // a tile's lse (log2 domain) and delta
+constexpr int kMaxRing = 5;
+constexpr int kDescRing = 4;
+constexpr int kDescReaders = 2 + kElemWarps;         // MMA, fix-up and elementwise warps
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kDCol = 256, kAcc0 = 384, kAcc1 = 448;
+constexpr float kLog2e = 1.4426950408889634f;
+
+// One work item as the producer publishes it (rows < 0: no further item).
+struct ItemDesc {
+    int f0, rows;   // owner rows
+    int s0, T;      // the segment
+    int h, kind;
+};
+
+struct Bars {
+    uint64_t own_full[2];
+    uint64_t own_empty[2];          // the item's last S and D MMAs have completed
+    uint64_t t_full[kMaxRing];
+    uint64_t t_ready[kMaxRing];     // the fix-up warp has checked the tile
+    uint64_t t_empty[kMaxRing];     // the tile's accumulating MMAs have completed
+    uint64_t s_full[2];
+    uint64_t s_empty[2];            // the accumulating MMAs that read P, dS have completed
+    uint64_t d_full;
+    uint64_t d_empty;               // kElemWarps arrivals: D has been read
+    uint64_t p_full[2];             // kElemWarps arrivals: P and dS written
+    uint64_t acc_full;              // the item's accumulators are complete
+    uint64_t mma_done;
+    uint64_t desc_full[kDescRing];
+    uint64_t desc_empty[kDescRing]; // kDescReaders arrivals
+    ItemDesc desc[kDescRing];
+    uint32_t tmem_base;
+    int abort_flag;
+};
+
+struct Params {
+    const int32_t *cu;
+    int n_seq;
+    int total;
+    int heads;
+    int block;          // frames per segment; 0: whole utterances
+    int xtiles;         // owner tiles per block (block mode)
+    int ring;
+    uint32_t ring_off, col_off, bars_off;
+    float scale, scale_log2;
+    const float *lse;   // [heads][total]
+    const float *delta; // [heads][total]
+    __nv_bfloat16 *dq, *dk, *dv;
+    long long out_stride;   // elements between gradient frames
+    int32_t *status;
+    unsigned long long wait_ns;
+    int flags;
+};
+
+__device__ __forceinline__ void tma_load(uint32_t dst, const void *tmap, int32_t x, int32_t y, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar)
+                 : "memory");
+}
+
+// The CTA's items in order: item i = blockIdx.x + n * gridDim.x =
+// ((u * X + x) * H + h) * 2 + c; u = 128-row unit of an utterance (X = 1), or
+// block, whose owner tile x may not exist.  The kind is c, flipped on odd n:
+// gridDim.x is even, so each CTA gets both kinds in turn and every (u, x, h)
+// both kinds once.
+struct ItemWalk {
+    PlanWalker w;
+    long long i;
+    int n;
+
+    __device__ __forceinline__ void init(const Params &p, int lane)
+    {
+        w.init(p.cu, p.n_seq, p.total, p.block ? p.block : kRows, lane);
+        i = blockIdx.x;
+        n = 0;
+    }
+
+    __device__ __forceinline__ bool next(const Params &p, int lane, ItemDesc &d)
+    {
+        for (;;) {
+            const long long uxh = i >> 1, ux = uxh / p.heads;
+            d.h = (int)(uxh - ux * p.heads);
+            d.kind = ((int)i ^ n) & 1;
+            i += gridDim.x;
+            ++n;
+            int f0, L, seq;
+            if (p.block) {
+                const long long u = ux / p.xtiles;
+                const int x = (int)(ux - u * p.xtiles);
+                if (!w.find(u, lane, f0, L, seq))
+                    return false;
+                if (x * kRows >= L)
+                    continue;
+                d.s0 = f0;
+                d.T = L;
+                d.f0 = f0 + x * kRows;
+                d.rows = min(kRows, L - x * kRows);
+            } else {
+                if (!w.find(ux, lane, f0, L, seq))
+                    return false;
+                d.s0 = __ldg(p.cu + seq);
+                d.T = __ldg(p.cu + seq + 1) - d.s0;
+                d.f0 = f0;
+                d.rows = L;
+            }
+            return true;
+        }
+    }
+};
+
+// A reader's walk over the published descriptors: waits for entry n.
+struct DescReader {
+    int n;
+    __device__ __forceinline__ bool next(Bars *bars, const Params &p, volatile int *abort_flag, ItemDesc &d)
+    {
+        const int j = n % kDescRing;
+        if (!wait_bar(smem_u32(&bars->desc_full[j]), (uint32_t)(n / kDescRing) & 1, abort_flag, p.wait_ns, p.status))
+            return false;
+        d = bars->desc[j];
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0)
+            mbar_arrive(smem_u32(&bars->desc_empty[j]));
+        ++n;
+        return d.rows >= 0;
+    }
+};
+
+// The tiles of an item that lie ahead of the MMA warp's accumulating side.
+struct Cursor {
+    ItemDesc d;
+    int tiles, j;   // tiles of the item; the current one
+};
+
+// 32 columns of the tile for this lane's row: P (in place of S's values).
+__device__ __forceinline__ void probs(float (&s)[64], int c0, float sl2, float row_lse2, const float *col_lse2,
+                                      bool by_col)
+{
+    if (by_col) {
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+            const float4 l = *reinterpret_cast<const float4 *>(col_lse2 + c0 + i);
+            s[c0 + i] = ex2_approx(fmaf(s[c0 + i], sl2, -l.x));
+            s[c0 + i + 1] = ex2_approx(fmaf(s[c0 + i + 1], sl2, -l.y));
+            s[c0 + i + 2] = ex2_approx(fmaf(s[c0 + i + 2], sl2, -l.z));
+            s[c0 + i + 3] = ex2_approx(fmaf(s[c0 + i + 3], sl2, -l.w));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            s[c0 + i] = ex2_approx(fmaf(s[c0 + i], sl2, -row_lse2));
+    }
+}
+
+// One tile for one lane: P and dS of the warpgroup's 64 columns.  nc: columns
+// of the MMA extent that lie in the warpgroup's half (a multiple of 16, > 0);
+// valid: columns inside the segment (kind 1 masks the others by index).
+template <bool kDQ>
+__device__ __forceinline__ bool elem_tile(uint32_t tS, uint32_t tD, int nc, int valid, float sl2, float row_lse2,
+                                          float row_delta, const float *col_lse2, const float *col_delta, Bars *bars,
+                                          uint32_t d_parity, const Params &p, volatile int *abort_flag)
+{
+    const int lane = threadIdx.x & 31;
+    float s[64];
+    uint32_t *su = reinterpret_cast<uint32_t *>(s);
+    const bool two = nc > 32;   // warp-uniform
+    tmem_ld32_nowait(tS, su);
+    if (two)
+        tmem_ld32_nowait(tS + 32, su + 32);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 64; ++i)
+        reg_fence(su[i]);
+#pragma unroll
+    for (int c0 = 0; c0 < 64; c0 += 32) {
+        if (c0 && !two)
+            break;
+        probs(s, c0, sl2, row_lse2, col_lse2, !kDQ);
+        if (kDQ && valid < c0 + 32) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                s[c0 + i] = c0 + i < valid ? s[c0 + i] : 0.f;
+        }
+        if (!kDQ) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                pk[i] = pack_bf16x2(s[c0 + 2 * i], s[c0 + 2 * i + 1]);
+            tmem_st16p(tS + c0 / 2, pk);
+        }
+    }
+    if (!wait_bar(smem_u32(&bars->d_full), d_parity, abort_flag, p.wait_ns, p.status))
+        return false;
+    tc_fence_after();
+#pragma unroll
+    for (int c0 = 0; c0 < 64; c0 += 32) {
+        if (c0 && !two)
+            break;
+        uint32_t d[32], pk[16];
+        tmem_ld32_nowait(tD + c0, d);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            reg_fence(d[i]);
+        if (c0 == 32 || !two) {   // D has been read
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(smem_u32(&bars->d_empty));
+        }
+        if (kDQ) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                // masked places: P is 0, but D may be anything
+                const float x = s[c0 + i] * (__uint_as_float(d[i]) - row_delta);
+                s[c0 + i] = valid < c0 + 32 && c0 + i >= valid ? 0.f : x;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+                const float4 dl = *reinterpret_cast<const float4 *>(col_delta + c0 + i);
+                s[c0 + i] *= __uint_as_float(d[i]) - dl.x;
+                s[c0 + i + 1] *= __uint_as_float(d[i + 1]) - dl.y;
+                s[c0 + i + 2] *= __uint_as_float(d[i + 2]) - dl.z;
+                s[c0 + i + 3] *= __uint_as_float(d[i + 3]) - dl.w;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            pk[i] = pack_bf16x2(s[c0 + 2 * i], s[c0 + 2 * i + 1]);
+        tmem_st16p(tS + 32 + c0 / 2, pk);
+    }
+    tmem_wait_st();
+    return true;
+}
+
+// `cols` columns of an accumulator row, times f, to bf16 at dst.
+__device__ __forceinline__ void store_acc(uint32_t tacc, int cols, float f, __nv_bfloat16 *dst, bool row_ok)
+{
+    for (int c = 0; c < cols; c += 32) {
+        uint32_t o[32];
+        tmem_ld32_nowait(tacc + c, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            reg_fence(o[i]);
+        if (row_ok) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8)
+                *reinterpret_cast<uint4 *>(dst + c + i) =
+                    make_uint4(pack_bf16x2(__uint_as_float(o[i]) * f, __uint_as_float(o[i + 1]) * f),
+                               pack_bf16x2(__uint_as_float(o[i + 2]) * f, __uint_as_float(o[i + 3]) * f),
+                               pack_bf16x2(__uint_as_float(o[i + 4]) * f, __uint_as_float(o[i + 5]) * f),
+                               pack_bf16x2(__uint_as_float(o[i + 6]) * f, __uint_as_float(o[i + 7]) * f));
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
+                    const Params p)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t own_base = smem_u32(smem);
+    const uint32_t ring_base = own_base + p.ring_off;
+    float *cols = reinterpret_cast<float *>(smem + p.col_off);   // per stage: lse2[128], delta[128]
+    Bars *bars = reinterpret_cast<Bars *>(smem + p.bars_off);
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int ring = p.ring;
+
+    // ------------------------------------------------------------ set-up
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(smem_u32(&bars->own_full[s]), 1);
+            mbar_init(smem_u32(&bars->own_empty[s]), 1);
+            mbar_init(smem_u32(&bars->s_full[s]), 1);
+            mbar_init(smem_u32(&bars->s_empty[s]), 1);
+            mbar_init(smem_u32(&bars->p_full[s]), kElemWarps);
+        }
+        for (int s = 0; s < ring; ++s) {
+            mbar_init(smem_u32(&bars->t_full[s]), 1);
+            mbar_init(smem_u32(&bars->t_ready[s]), 1);
+            mbar_init(smem_u32(&bars->t_empty[s]), 1);
+        }
+        mbar_init(smem_u32(&bars->d_full), 1);
+        mbar_init(smem_u32(&bars->d_empty), kElemWarps);
+        mbar_init(smem_u32(&bars->acc_full), 1);
+        mbar_init(smem_u32(&bars->mma_done), 1);
+        for (int j = 0; j < kDescRing; ++j) {
+            mbar_init(smem_u32(&bars->desc_full[j]), 1);
+            mbar_init(smem_u32(&bars->desc_empty[j]), kDescReaders);
+        }
+        bars->abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 3) {
+        tmem_alloc(smem_u32(&bars->tmem_base), kTmemCols);
+        tmem_relinquish();
+    }
+    if (threadIdx.x == 64) {
+        tma_prefetch_desc(&tm_q);
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
+        tma_prefetch_desc(&tm_do);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem_base;
+    volatile int *abort_flag = &bars->abort_flag;
+    const unsigned long long wait_ns = p.wait_ns;
+
+    if (warp == 0) {
+        // ======================================================== producer
+        ItemWalk it;
+        it.init(p, lane);
+        const bool skip0 = (p.flags & NLE_FLAG_TEST_SKIP_FIRST_LOAD) != 0;
+        int n = 0;    // items published
+        int nown = 0; // owner stages claimed
+        int nt = 0;   // tiles claimed
+        bool stop = false;
+        auto publish = [&](const ItemDesc &d) -> bool {
+            const int j = n % kDescRing;
+            if (n >= kDescRing && !wait_bar(smem_u32(&bars->desc_empty[j]), (uint32_t)(n / kDescRing - 1) & 1,
+                                            abort_flag, wait_ns, p.status))
+                return false;
+            if (lane == 0) {
+                bars->desc[j] = d;
+                mbar_arrive(smem_u32(&bars->desc_full[j]));
+            }
+            __syncwarp();
+            ++n;
+            return true;
+        };
+        ItemDesc d;
+        while (!stop && it.next(p, lane, d)) {
+            if (!publish(d)) {
+                stop = true;
+                break;
+            }
+            const int os = nown & 1;
+            if (nown >= 2 && !wait_bar(smem_u32(&bars->own_empty[os]), (uint32_t)((nown >> 1) - 1) & 1, abort_flag,
+                                       wait_ns, p.status)) {
+                stop = true;
+                break;
+            }
+            if (lane == 0 && !(skip0 && nown == 0)) {
+                const uint32_t bar = smem_u32(&bars->own_full[os]);
+                const uint32_t dst = own_base + os * kPairBytes;
+                mbar_arrive_expect_tx(bar, kPairBytes);
+                tma_load(dst, d.kind ? &tm_q : &tm_k, d.h * 64, d.f0, bar);
+                tma_load(dst + kMatBytes, d.kind ? &tm_do : &tm_v, d.h * 64, d.f0, bar);
+            }
+            __syncwarp();
+            ++nown;
+            for (int j = 0; j * kRows < d.T; ++j) {
+                const int s = nt % ring;
+                const uint32_t u = (uint32_t)(nt / ring);
+                if (u > 0 && !wait_bar(smem_u32(&bars->t_empty[s]), (u - 1) & 1, abort_flag, wait_ns, p.status)) {
+                    stop = true;
+                    break;
+                }
+                if (lane == 0) {
+                    const uint32_t bar = smem_u32(&bars->t_full[s]);
+                    const uint32_t dst = ring_base + s * kPairBytes;
+                    mbar_arrive_expect_tx(bar, kPairBytes);
+                    tma_load(dst, d.kind ? &tm_k : &tm_q, d.h * 64, d.s0 + j * kRows, bar);
+                    tma_load(dst + kMatBytes, d.kind ? &tm_v : &tm_do, d.h * 64, d.s0 + j * kRows, bar);
+                }
+                __syncwarp();
+                ++nt;
+            }
+        }
+        if (it.w.bad && lane == 0)
+            report(p.status, NLE_ERR_INVALID_ARG);
+        if (!stop)
+            publish(ItemDesc{0, -1, 0, 0, 0, 0});
+        // drain: the last copy into each stage must land before exit
+        if (lane == 0) {
+            for (int m = nown - 2; m < nown; ++m)
+                if (m >= 0 && !(skip0 && m == 0))
+                    wait_bar_drain(smem_u32(&bars->own_full[m & 1]), (uint32_t)(m >> 1) & 1, wait_ns);
+            for (int m = nt - ring; m < nt; ++m)
+                if (m >= 0)
+                    wait_bar_drain(smem_u32(&bars->t_full[m % ring]), (uint32_t)(m / ring) & 1, wait_ns);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ======================================================== MMA issuer
+        DescReader rd{0};
+        Cursor front{}, back{};
+        int tf = 0, tb = 0;  // tiles issued by the front (S, D) and the back (accumulators)
+        int nown = 0;        // items entered by the front
+        bool ok = true;
+        bool more = rd.next(bars, p, abort_flag, front.d);
+        const uint32_t id_acc = idesc_bf16_f32(128, 64, true);
+
+        auto enter = [&]() -> bool {   // the front's item: its owner tile must have landed
+            front.tiles = (front.d.T + kRows - 1) / kRows;
+            front.j = 0;
+            const int os = nown & 1;
+            return wait_bar(smem_u32(&bars->own_full[os]), (uint32_t)(nown >> 1) & 1, abort_flag, wait_ns, p.status);
+        };
+        auto front_issue = [&]() -> bool {   // S and D of the front's tile
+            const int s = tf % ring, b = tf & 1;
+            const uint32_t u = (uint32_t)tf >> 1;   // uses of S buffer b before this one
+            if (!wait_bar(smem_u32(&bars->t_ready[s]), (uint32_t)(tf / ring) & 1, abort_flag, wait_ns, p.status))
+                return false;
+            if (u > 0 && !wait_bar(smem_u32(&bars->s_empty[b]), (u - 1) & 1, abort_flag, wait_ns, p.status))
+                return false;
+            tc_fence_after();
+            const int nv = min(kRows, front.d.T - front.j * kRows);
+            const uint32_t id = idesc_bf16_f32(128, (nv + 15) & ~15, false);
+            const uint32_t xo = own_base + (nown & 1) * kPairBytes, xt = ring_base + s * kPairBytes;
+            {
+                const uint64_t da = smem_desc_sw128(xo, 16, 1024), db = smem_desc_sw128(xt, 16, 1024);
+                if (elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_ss(tmem + b * 128, da + 2 * kk, db + 2 * kk, id, kk > 0 ? 1u : 0u);
+                    mma_commit(smem_u32(&bars->s_full[b]));
+                }
+                __syncwarp();
+            }
+            if (tf > 0 &&
+                !wait_bar(smem_u32(&bars->d_empty), (uint32_t)(tf - 1) & 1, abort_flag, wait_ns, p.status))
+                return false;
+            tc_fence_after();
+            {
+                const uint64_t da = smem_desc_sw128(xo + kMatBytes, 16, 1024),
+                               db = smem_desc_sw128(xt + kMatBytes, 16, 1024);
+                if (elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_ss(tmem + kDCol, da + 2 * kk, db + 2 * kk, id, kk > 0 ? 1u : 0u);
+                    mma_commit(smem_u32(&bars->d_full));
+                    if (front.j == front.tiles - 1)   // the item's last use of its owner tile
+                        mma_commit(smem_u32(&bars->own_empty[nown & 1]));
+                }
+                __syncwarp();
+            }
+            ++tf;
+            return true;
+        };
+        auto back_issue = [&]() -> bool {   // the accumulating MMAs of the back's tile
+            const int s = tb % ring, b = tb & 1;
+            if (!wait_bar(smem_u32(&bars->p_full[b]), ((uint32_t)tb >> 1) & 1, abort_flag, wait_ns, p.status))
+                return false;
+            tc_fence_after();
+            const int nv = min(kRows, back.d.T - back.j * kRows);
+            const int steps = (nv + 15) >> 4;
+            const uint32_t xt = ring_base + s * kPairBytes;
+            // N = 64 is one 128-byte swizzle atom along N; K steps of 16
+            // rows advance the start by 2048 bytes
+            const uint64_t dx = smem_desc_sw128(xt, 0, 1024), dy = smem_desc_sw128(xt + kMatBytes, 0, 1024);
+            if (elect_one()) {
+                const uint32_t sb = tmem + b * 128;
+                for (int kk = 0; kk < steps; ++kk) {
+                    const uint32_t a = sb + (kk >> 2) * 64 + (kk & 3) * 8;
+                    const uint32_t acc = back.j > 0 || kk > 0 ? 1u : 0u;
+                    const uint64_t row = (uint64_t)(kk * (16 * kRowBytes >> 4));
+                    if (back.d.kind == 0)
+                        mma_ts(tmem + kAcc1, a, dy + row, id_acc, acc);
+                    mma_ts(tmem + kAcc0, a + 32, dx + row, id_acc, acc);
+                }
+                mma_commit(smem_u32(&bars->t_empty[s]));
+                mma_commit(smem_u32(&bars->s_empty[b]));
+                if (back.j == back.tiles - 1)
+                    mma_commit(smem_u32(&bars->acc_full));
+            }
+            __syncwarp();
+            ++tb;
+            return true;
+        };
+
+        if (more) {
+            ok = enter() && front_issue();
+            back = front;
+            while (ok) {
+                // the front moves one tile on: the next of its item, or the next item's first
+                bool ahead = false;   // the front is at a tile that has been issued and the back has not reached
+                if (front.j + 1 < front.tiles) {
+                    ++front.j;
+                    ahead = true;
+                } else {
+                    ++nown;
+                    ahead = more = rd.next(bars, p, abort_flag, front.d);
+                    if (!more && *abort_flag) {
+                        ok = false;
+                        break;
+                    }
+                    if (more)
+                        ok = enter();
+                }
+                if (ok && ahead)
+                    ok = front_issue();
+                if (!ok || !back_issue())
+                    break;
+                if (!ahead)
+                    break;
+                back = front;
+            }
+        }
+        // every MMA must finish before TMEM is released
+        if (elect_one()) {
+            mma_commit(smem_u32(&bars->mma_done));
+            wait_bar_drain(smem_u32(&bars->mma_done), 0, wait_ns);
+        }
+        __syncwarp();
+    } else if (warp == 2) {
+        // ======================================================== tile fix-up
+        DescReader rd{0};
+        ItemDesc d;
+        int nt = 0;
+        bool ok = true;
+        while (ok && rd.next(bars, p, abort_flag, d)) {
+            for (int j = 0; j * kRows < d.T; ++j, ++nt) {
+                const int s = nt % ring;
+                const int nv = min(kRows, d.T - j * kRows);
+                const int nk = (nv + 15) & ~15;
+                float l[4], dl[4];
+                if (d.kind == 0) {
+                    const size_t at = (size_t)d.h * p.total + d.s0 + j * kRows;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int c = lane + 32 * i;
+                        l[i] = c < nv ? __ldg(p.lse + at + c) * kLog2e : INFINITY;
+                        dl[i] = c < nv ? __ldg(p.delta + at + c) : 0.f;
+                    }
+                }
+                if (!wait_bar(smem_u32(&bars->t_full[s]), (uint32_t)(nt / ring) & 1, abort_flag, wait_ns, p.status)) {
+                    ok = false;
+                    break;
+                }
+                if (d.kind == 0) {
+                    float *cl = cols + s * (2 * kRows);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        cl[lane + 32 * i] = l[i];
+                        cl[kRows + lane + 32 * i] = dl[i];
+                    }
+                }
+                if (nv < nk) {
+                    for (int m = 0; m < 2; ++m) {
+                        uint4 *z = reinterpret_cast<uint4 *>(smem + p.ring_off + s * kPairBytes + m * kMatBytes +
+                                                             nv * kRowBytes);
+                        for (int i = lane; i < (nk - nv) * (kRowBytes / 16); i += 32)
+                            z[i] = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_u32(&bars->t_ready[s]));
+            }
+        }
+    } else if (warp >= kElem0) {
+        // ======================================================== elementwise
+        const int g = (warp - kElem0) >> 2;   // warpgroup: columns 64g..64g+63
+        const int qq = warp & 3;              // TMEM lane quarter of this warp
+        const uint32_t lanes = (uint32_t)(qq * 32) << 16;
+        const float sl2 = p.scale_log2;
+        DescReader rd{0};
+        ItemDesc d;
+        int nt = 0, n = 0;
+        bool ok = true;
+        for (; ok && rd.next(bars, p, abort_flag, d); ++n) {
+            const int row = qq * 32 + lane;
+            const bool active = qq * 32 < d.rows;   // warp-uniform
+            const bool row_ok = row < d.rows;
+            float row_lse2 = 0.f, row_delta = 0.f;
+            if (d.kind == 1 && row_ok) {
+                const size_t at = (size_t)d.h * p.total + d.f0 + row;
+                row_lse2 = __ldg(p.lse + at) * kLog2e;
+                row_delta = __ldg(p.delta + at);
+            }
+            const int tiles = (d.T + kRows - 1) / kRows;
+            for (int j = 0; j < tiles; ++j, ++nt) {
+                const int b = nt & 1, s = nt % ring;
+                const int nv = min(kRows, d.T - j * kRows);
+                const int nc = ((nv + 15) & ~15) - 64 * g;   // MMA columns in this warpgroup's half
+                // the tile's lse and delta (kind 0) were staged before this
+                if (!wait_bar(smem_u32(&bars->t_ready[s]), (uint32_t)(nt / ring) & 1, abort_flag, wait_ns, p.status) ||
+                    !wait_bar(smem_u32(&bars->s_full[b]), ((uint32_t)nt >> 1) & 1, abort_flag, wait_ns, p.status)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                if (active && nc > 0) {
+                    const uint32_t tS = tmem + b * 128 + 64 * g + lanes, tD = tmem + kDCol + 64 * g + lanes;
+                    const float *cl = cols + s * (2 * kRows) + 64 * g;
+                    ok = d.kind ? elem_tile<true>(tS, tD, nc, nv - 64 * g, sl2, row_lse2, row_delta, cl, cl + kRows,
+                                                  bars, (uint32_t)nt & 1, p, abort_flag)
+                                : elem_tile<false>(tS, tD, nc, nv - 64 * g, sl2, row_lse2, row_delta, cl, cl + kRows,
+                                                   bars, (uint32_t)nt & 1, p, abort_flag);
+                } else {
+                    ok = wait_bar(smem_u32(&bars->d_full), (uint32_t)nt & 1, abort_flag, wait_ns, p.status);
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(smem_u32(&bars->d_empty));
+                }
+                if (!ok)
+                    break;
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_u32(&bars->p_full[b]));
+            }
+            if (!ok)
+                break;
+            // ---------------------------------------------- output rows
+            if (!wait_bar(smem_u32(&bars->acc_full), (uint32_t)n & 1, abort_flag, wait_ns, p.status))
+                break;
+            tc_fence_after();
+            if (active) {
+                const long long at = (long long)(d.f0 + row) * p.out_stride + d.h * 64;
+                if (d.kind)
+                    store_acc(tmem + kAcc0 + 32 * g + lanes, 32, p.scale, p.dq + at + 32 * g, row_ok);
+                else if (g == 0)
+                    store_acc(tmem + kAcc0 + lanes, 64, p.scale, p.dk + at, row_ok);
+                else
+                    store_acc(tmem + kAcc1 + lanes, 64, 1.f, p.dv + at, row_ok);
+            }
+            tc_fence_before();
+        }
+    }
+
+    // ------------------------------------------------------------ teardown
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 3) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// delta[h][f] = sum_d dO O (fp32): eight lanes per head row, four heads of a
+// frame per warp load.  Memory-bound: reads O and dO once.
+__global__ void __launch_bounds__(256)
+    attn_delta_kernel(const uint4 *out, const uint4 *dout, long long dout_stride, float *delta, int total, int heads)
+{
+    const int lane = threadIdx.x & 31;
+    const long long rows = (long long)total * heads;
+    for (long long r0 = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * 4; r0 < rows; r0 += (long long)gridDim.x * 32) {
+        const long long r = r0 + (lane >> 3);
+        float s = 0.f;
+        int f = 0, h = 0;
+        if (r < rows) {
+            f = (int)(r / heads);
+            h = (int)(r - (long long)f * heads);
+            const uint4 a = __ldg(out + r * 8 + (lane & 7));
+            const uint4 b = __ldg(dout + (f * dout_stride + (long long)h * 64) / 8 + (lane & 7));
+            const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                s = fmaf(__uint_as_float(av[i] << 16), __uint_as_float(bv[i] << 16), s);
+                s = fmaf(__uint_as_float(av[i] & 0xffff0000u), __uint_as_float(bv[i] & 0xffff0000u), s);
+            }
+        }
+        s += __shfl_xor_sync(kFull, s, 1);
+        s += __shfl_xor_sync(kFull, s, 2);
+        s += __shfl_xor_sync(kFull, s, 4);
+        if (r < rows && (lane & 7) == 0)
+            delta[(size_t)h * total + f] = s;
+    }
+}
+
+// block = 0: whole utterances.
+int launch_attn_bwd(const nle_attn_bwd_args *a, int block, void *stream)
+{
+    if (!a || a->n_seq < 0 || a->total_frames < 0 || a->heads <= 0 || block < 0 || a->wait_limit_ns < 0)
+        return NLE_ERR_INVALID_ARG;
+    if (a->d_head != 64 || block > 256 || a->total_frames > 0x7fffffffLL)
+        return NLE_ERR_UNSUPPORTED;
+    const int xtiles = block ? (block + kRows - 1) / kRows : 1;
+    // upper bound on work items: two kinds, each utterance at most T/unit + 1 units
+    const long long units = a->n_seq + a->total_frames / (block ? block : kRows);
+    if (units > 0x7fffffffLL || units * xtiles * 2 > 0x7fffffffLL / a->heads)
+        return NLE_ERR_UNSUPPORTED;
+    if (a->n_seq == 0 || a->total_frames == 0)
+        return NLE_OK;
+    const void *ptrs[] = {a->q, a->k, a->v, a->out, a->dout, a->dq, a->dk, a->dv, a->lse, a->cu_seqlens, a->workspace};
+    for (const void *x : ptrs)
+        if (!x)
+            return NLE_ERR_INVALID_ARG;
+    const int64_t dense = (int64_t)a->heads * 64;
+    const int64_t stride = a->row_stride_qkv ? a->row_stride_qkv : dense;
+    const int64_t dstride = a->row_stride_dqkv ? a->row_stride_dqkv : dense;
+    if (stride < dense || dstride < dense || dense > 0x7fffffffLL || stride > (1ll << 38) || dstride > (1ll << 38))
+        return NLE_ERR_INVALID_ARG;
+    if (stride % 8 != 0 || dstride % 8 != 0)
+        return NLE_ERR_MISALIGNED;
+    for (int i = 0; i < 8; ++i)
+        if (!nle::aligned16(ptrs[i]))
+            return NLE_ERR_MISALIGNED;
+
+    nle::DeviceInfo di;
+    int dev = 0;
+    if (!nle::current_device_info(&di, &dev))
+        return NLE_ERR_CUDA;
+    if (di.cc_major != 10)
+        return NLE_ERR_UNSUPPORTED;
+    const long long items = units * xtiles * 2 * a->heads;
+    // an even grid: the two kinds of an owner tile are taken in the same round
+    const int grid = (int)(items < (di.sm_count & ~1) ? items : (di.sm_count & ~1));
+    // the kernel counts the tiles that a CTA walks in 32 bits
+    if ((items / grid + 1) * ((block ? block : a->total_frames) / kRows + 1) > 0x7fffffffLL)
+        return NLE_ERR_UNSUPPORTED;
+
+    Params p{};
+    p.cu = a->cu_seqlens;
+    p.n_seq = a->n_seq;
+    p.total = (int)a->total_frames;
+    p.heads = a->heads;
+    p.block = block;
+    p.xtiles = xtiles;
+    const size_t bars_bytes = ((sizeof(Bars) + 127) / 128) * 128 + 1024;
+    int ring = (int)(((size_t)di.smem_optin - 2 * kPairBytes - bars_bytes) / (kPairBytes + kColBytes));
+    if (ring > kMaxRing)
+        ring = kMaxRing;
+    if (ring < 2)
+        return NLE_ERR_UNSUPPORTED;
+    p.ring = ring;
+    p.ring_off = 2 * kPairBytes;
+    p.col_off = p.ring_off + (uint32_t)ring * kPairBytes;
+    p.bars_off = p.col_off + (uint32_t)ring * kColBytes;
+    const size_t smem = p.bars_off + bars_bytes;   // above half the SM's: one CTA per SM (it owns all TMEM)
+    const double scale = a->softmax_scale > 0.f ? (double)a->softmax_scale : 1.0 / std::sqrt((double)a->d_head);
+    p.scale = (float)scale;
+    p.scale_log2 = (float)(scale * 1.4426950408889634);
+    p.lse = a->lse;
+    p.delta = static_cast<const float *>(a->workspace);
+    p.dq = static_cast<__nv_bfloat16 *>(a->dq);
+    p.dk = static_cast<__nv_bfloat16 *>(a->dk);
+    p.dv = static_cast<__nv_bfloat16 *>(a->dv);
+    p.out_stride = dstride;
+    p.status = a->dev_status;
+    p.wait_ns = a->wait_limit_ns > 0 ? (unsigned long long)a->wait_limit_ns : 1000000000ull;
+    p.flags = a->flags;
+
+    CUtensorMap tq, tk, tv, tdo;
+    const uint64_t cols = (uint64_t)dense, rows = (uint64_t)a->total_frames;
+    if (!nle::encode_tmap_bf16_2d(&tq, a->q, cols, rows, stride, 64, kRows) ||
+        !nle::encode_tmap_bf16_2d(&tk, a->k, cols, rows, stride, 64, kRows) ||
+        !nle::encode_tmap_bf16_2d(&tv, a->v, cols, rows, stride, 64, kRows) ||
+        !nle::encode_tmap_bf16_2d(&tdo, a->dout, cols, rows, dense, 64, kRows))
+        return NLE_ERR_CUDA;
+    if (!nle::allow_max_dynamic_smem(reinterpret_cast<const void *>(attn_bwd_kernel), dev, di.smem_optin))
+        return NLE_ERR_CUDA;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const long long drows = a->total_frames * (long long)a->heads;
+    const long long dgrid = (drows + 31) / 32;
+    attn_delta_kernel<<<(unsigned)(dgrid < 16ll * di.sm_count ? dgrid : 16ll * di.sm_count), 256, 0, st>>>(
+        static_cast<const uint4 *>(a->out), static_cast<const uint4 *>(a->dout), dense,
+        static_cast<float *>(a->workspace), p.total, a->heads);
+    if (cudaGetLastError() != cudaSuccess)
+        return NLE_ERR_CUDA;
+    attn_bwd_kernel<<<grid, kThreads, smem, st>>>(tq, tk, tv, tdo, p);
+    return cudaGetLastError() == cudaSuccess ? NLE_OK : NLE_ERR_CUDA;
+}
+
+} // namespace
+
+extern "C" int nle_block_attn_bwd(const nle_attn_bwd_args *args, int block_frames, void *stream)
+{
+    if (block_frames <= 0)
+        return NLE_ERR_INVALID_ARG;
+    return launch_attn_bwd(args, block_frames, stream);
+}
+
+extern "C" int nle_varlen_attn_bwd(const nle_attn_bwd_args *args, void *stream)
+{
+    return launch_attn_bwd(args, 0, stream);
+}

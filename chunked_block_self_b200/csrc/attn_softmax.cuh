@@ -214,8 +214,9 @@ __device__ __forceinline__ void softmax_step(uint32_t tS, int L, float sl2, floa
 // (the block kernels).  Returns this lane's row sum; P (bf16) is left over
 // the first NB/2 columns of S.  Segments wholly at or past L are skipped (the MMAs stop at
 // ceil16(L) keys).
+// m: the row's shift (log2 domain), so that log2(sum exp2(x)) = m + log2(l).
 template <int NB, int SEG>
-__device__ __forceinline__ float block_softmax_rows(uint32_t tS, int L, float sl2)
+__device__ __forceinline__ float block_softmax_rows(uint32_t tS, int L, float sl2, float &m)
 {
     static_assert(SEG % 16 == 0 && SEG >= 16, "segments");
     constexpr int W0 = NB < SEG ? NB : SEG;
@@ -226,7 +227,7 @@ __device__ __forceinline__ float block_softmax_rows(uint32_t tS, int L, float sl
     // first shift: max of the first 16 keys (keys >= L masked first)
     if (W0 > L)
         seg_mask<W0>(buf, 0, L);
-    float m = fmax3(fmax3(__uint_as_float(buf[0]), __uint_as_float(buf[1]), __uint_as_float(buf[2])),
+    m = fmax3(fmax3(__uint_as_float(buf[0]), __uint_as_float(buf[1]), __uint_as_float(buf[2])),
                     fmax3(__uint_as_float(buf[3]), __uint_as_float(buf[4]), __uint_as_float(buf[5])),
                     fmax3(__uint_as_float(buf[6]), __uint_as_float(buf[7]), __uint_as_float(buf[8])));
     m = fmax3(m, fmax3(__uint_as_float(buf[9]), __uint_as_float(buf[10]), __uint_as_float(buf[11])),
@@ -237,6 +238,19 @@ __device__ __forceinline__ float block_softmax_rows(uint32_t tS, int L, float sl
     softmax_step<NB, SEG, 0>(tS, L, sl2, m, l, buf);
     tmem_wait_st();
     return l;
+}
+
+template <int NB, int SEG>
+__device__ __forceinline__ float block_softmax_rows(uint32_t tS, int L, float sl2)
+{
+    float m;
+    return block_softmax_rows<NB, SEG>(tS, L, sl2, m);
+}
+
+// Natural log of a row's sum of exp(scale * s), from its shift and sum.
+__device__ __forceinline__ float row_lse(float m, float l)
+{
+    return fmaf(m, 0.693147180559945309f, logf(l));
 }
 
 } // namespace nle

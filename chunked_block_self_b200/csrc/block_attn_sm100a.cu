@@ -126,6 +126,7 @@ struct Params {
     float scale_log2;
     __nv_bfloat16 *out;
     int out_stride;     // elements between output frames (heads * 64)
+    float *lse;         // [heads][total] (kLse kernels only)
     int32_t *status;
     unsigned long long wait_ns;
     int flags;
@@ -171,7 +172,8 @@ struct ItemSeq {
     }
 };
 
-template <int NB>
+// kLse: every row's log-sum-exp is written too (kept for a backward pass).
+template <int NB, bool kLse>
 __global__ void __launch_bounds__(kThreads, 1)
     block_attn_kernel(const __grid_constant__ CUtensorMap tm_q0, const __grid_constant__ CUtensorMap tm_q1,
                       const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const Params p)
@@ -427,8 +429,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int row0 = x * kQTile + qq * 32;   // first block row of this warp
             const bool active = row0 < L;
             float l = 1.f;
-            if (active)
-                l = block_softmax_rows<NB, kSeg>(tS, L, sl2);
+            if (active) {
+                if constexpr (kLse) {
+                    float m;
+                    l = block_softmax_rows<NB, kSeg>(tS, L, sl2, m);
+                    if (row0 + lane < L)
+                        p.lse[(size_t)hcur * p.total + f0 + row0 + lane] = row_lse(m, l);
+                } else {
+                    l = block_softmax_rows<NB, kSeg>(tS, L, sl2);
+                }
+            }
             if (lane == 0 && qq == 0)
                 NLE_TRACE_AT(3 + t, n * 2 + x, 1);
             tc_fence_before();
@@ -533,39 +543,38 @@ struct KernelInfo {
 };
 
 template <int NB>
-KernelInfo kernel_nb()
+KernelInfo kernel_nb(bool lse)
 {
-    return {reinterpret_cast<BlockKernel>(block_attn_kernel<NB>)};
+    return {lse ? reinterpret_cast<BlockKernel>(block_attn_kernel<NB, true>)
+                : reinterpret_cast<BlockKernel>(block_attn_kernel<NB, false>)};
 }
 
-KernelInfo pick_kernel(int nb)
+KernelInfo pick_kernel(int nb, bool lse)
 {
     switch (nb) {
-    case 16: return kernel_nb<16>();
-    case 32: return kernel_nb<32>();
-    case 48: return kernel_nb<48>();
-    case 64: return kernel_nb<64>();
-    case 80: return kernel_nb<80>();
-    case 96: return kernel_nb<96>();
-    case 112: return kernel_nb<112>();
-    case 128: return kernel_nb<128>();
-    case 144: return kernel_nb<144>();
-    case 160: return kernel_nb<160>();
-    case 176: return kernel_nb<176>();
-    case 192: return kernel_nb<192>();
-    case 208: return kernel_nb<208>();
-    case 224: return kernel_nb<224>();
-    case 240: return kernel_nb<240>();
-    default: return kernel_nb<256>();
+    case 16: return kernel_nb<16>(lse);
+    case 32: return kernel_nb<32>(lse);
+    case 48: return kernel_nb<48>(lse);
+    case 64: return kernel_nb<64>(lse);
+    case 80: return kernel_nb<80>(lse);
+    case 96: return kernel_nb<96>(lse);
+    case 112: return kernel_nb<112>(lse);
+    case 128: return kernel_nb<128>(lse);
+    case 144: return kernel_nb<144>(lse);
+    case 160: return kernel_nb<160>(lse);
+    case 176: return kernel_nb<176>(lse);
+    case 192: return kernel_nb<192>(lse);
+    case 208: return kernel_nb<208>(lse);
+    case 224: return kernel_nb<224>(lse);
+    case 240: return kernel_nb<240>(lse);
+    default: return kernel_nb<256>(lse);
     }
 }
 
-} // namespace
-
-extern "C" int nle_block_attn_fwd_ex(const void *q, const void *k, const void *v, void *out,
-                                     const int32_t *cu_seqlens, int n_seq, int64_t total_frames, int heads,
-                                     int d_head, int block_frames, float softmax_scale, int64_t row_stride_qkv,
-                                     int32_t *dev_status, int flags, int64_t wait_limit_ns, void *stream)
+// lse: null, or where every row's log-sum-exp goes.
+int launch_block_attn(const void *q, const void *k, const void *v, void *out, float *lse, const int32_t *cu_seqlens,
+                      int n_seq, int64_t total_frames, int heads, int d_head, int block_frames, float softmax_scale,
+                      int64_t row_stride_qkv, int32_t *dev_status, int flags, int64_t wait_limit_ns, void *stream)
 {
     if (n_seq < 0 || total_frames < 0 || heads <= 0 || block_frames <= 0 || wait_limit_ns < 0)
         return NLE_ERR_INVALID_ARG;
@@ -663,12 +672,35 @@ extern "C" int nle_block_attn_fwd_ex(const void *q, const void *k, const void *v
     const long long work = p.split ? 2 * items_bound : max_items;
     if (p.split && 2 * items_bound > 0x7fffffffLL)
         return NLE_ERR_UNSUPPORTED;
-    const KernelInfo kern = pick_kernel(NB);
+    p.lse = lse;
+    const KernelInfo kern = pick_kernel(NB, lse != nullptr);
     if (!nle::allow_max_dynamic_smem(reinterpret_cast<const void *>(kern.fn), dev, di.smem_optin))
         return NLE_ERR_CUDA;
     const int grid = (int)(work < di.sm_count ? work : di.sm_count);
     kern.fn<<<grid, kThreads, smem, static_cast<cudaStream_t>(stream)>>>(tq0, tq1, tk, tv, p);
     return cudaGetLastError() == cudaSuccess ? NLE_OK : NLE_ERR_CUDA;
+}
+
+} // namespace
+
+extern "C" int nle_block_attn_fwd_ex(const void *q, const void *k, const void *v, void *out,
+                                     const int32_t *cu_seqlens, int n_seq, int64_t total_frames, int heads,
+                                     int d_head, int block_frames, float softmax_scale, int64_t row_stride_qkv,
+                                     int32_t *dev_status, int flags, int64_t wait_limit_ns, void *stream)
+{
+    return launch_block_attn(q, k, v, out, nullptr, cu_seqlens, n_seq, total_frames, heads, d_head, block_frames,
+                             softmax_scale, row_stride_qkv, dev_status, flags, wait_limit_ns, stream);
+}
+
+extern "C" int nle_block_attn_fwd_lse(const void *q, const void *k, const void *v, void *out, float *lse,
+                                      const int32_t *cu_seqlens, int n_seq, int64_t total_frames, int heads,
+                                      int d_head, int block_frames, float softmax_scale, int64_t row_stride_qkv,
+                                      int32_t *dev_status, int flags, int64_t wait_limit_ns, void *stream)
+{
+    if (!lse && n_seq > 0 && total_frames > 0)
+        return NLE_ERR_INVALID_ARG;
+    return launch_block_attn(q, k, v, out, lse, cu_seqlens, n_seq, total_frames, heads, d_head, block_frames,
+                             softmax_scale, row_stride_qkv, dev_status, flags, wait_limit_ns, stream);
 }
 
 extern "C" int nle_block_attn_fwd(const void *q, const void *k, const void *v, void *out, const int32_t *cu_seqlens,

@@ -113,6 +113,7 @@ struct Params {
     float scale_log2;
     __nv_bfloat16 *out;
     int out_stride;     // elements between output frames (heads * 64)
+    float *lse;         // [heads][total] (kLse kernel only)
     int32_t *status;
     unsigned long long wait_ns;
     int flags;
@@ -280,6 +281,8 @@ __device__ __forceinline__ void rescale_o(uint32_t tO, float f)
     tmem_wait_st();
 }
 
+// kLse: every row's log-sum-exp is written too (kept for a backward pass).
+template <bool kLse>
 __global__ void __launch_bounds__(kThreads, 1)
     varlen_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const Params p)
@@ -599,6 +602,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool row_ok = row0 + lane < L;
                 const int f0 = bars->desc[dj].f0, h = bars->desc[dj].h;
                 uint4 *dst = reinterpret_cast<uint4 *>(p.out + (size_t)(f0 + row0 + lane) * p.out_stride + h * 64);
+                if constexpr (kLse) {
+                    if (row_ok)
+                        p.lse[(size_t)h * p.total + f0 + row0 + lane] = row_lse(m, l);
+                }
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     uint32_t o[32];
@@ -642,12 +649,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-} // namespace
-
-extern "C" int nle_varlen_attn_fwd_ex(const void *q, const void *k, const void *v, void *out,
-                                      const int32_t *cu_seqlens, int n_seq, int64_t total_frames, int heads,
-                                      int d_head, float softmax_scale, int64_t row_stride_qkv, int32_t *dev_status,
-                                      int flags, int64_t wait_limit_ns, void *stream)
+// lse: null, or where every row's log-sum-exp goes.
+int launch_varlen_attn(const void *q, const void *k, const void *v, void *out, float *lse, const int32_t *cu_seqlens,
+                       int n_seq, int64_t total_frames, int heads, int d_head, float softmax_scale,
+                       int64_t row_stride_qkv, int32_t *dev_status, int flags, int64_t wait_limit_ns, void *stream)
 {
     if (n_seq < 0 || total_frames < 0 || heads <= 0 || wait_limit_ns < 0)
         return NLE_ERR_INVALID_ARG;
@@ -716,11 +721,35 @@ extern "C" int nle_varlen_attn_fwd_ex(const void *q, const void *k, const void *
         !nle::encode_tmap_bf16_2d(&tv, v, cols, rows, stride, 64, kKeys))
         return NLE_ERR_CUDA;
 
-    if (!nle::allow_max_dynamic_smem(reinterpret_cast<const void *>(varlen_attn_kernel), dev, di.smem_optin))
+    p.lse = lse;
+    const auto kern = lse ? varlen_attn_kernel<true> : varlen_attn_kernel<false>;
+    if (!nle::allow_max_dynamic_smem(reinterpret_cast<const void *>(kern), dev, di.smem_optin))
         return NLE_ERR_CUDA;
     const int grid = (int)grid_ll;
-    varlen_attn_kernel<<<grid, kThreads, smem, static_cast<cudaStream_t>(stream)>>>(tq, tk, tv, p);
+    kern<<<grid, kThreads, smem, static_cast<cudaStream_t>(stream)>>>(tq, tk, tv, p);
     return cudaGetLastError() == cudaSuccess ? NLE_OK : NLE_ERR_CUDA;
+}
+
+} // namespace
+
+extern "C" int nle_varlen_attn_fwd_ex(const void *q, const void *k, const void *v, void *out,
+                                      const int32_t *cu_seqlens, int n_seq, int64_t total_frames, int heads,
+                                      int d_head, float softmax_scale, int64_t row_stride_qkv, int32_t *dev_status,
+                                      int flags, int64_t wait_limit_ns, void *stream)
+{
+    return launch_varlen_attn(q, k, v, out, nullptr, cu_seqlens, n_seq, total_frames, heads, d_head, softmax_scale,
+                              row_stride_qkv, dev_status, flags, wait_limit_ns, stream);
+}
+
+extern "C" int nle_varlen_attn_fwd_lse(const void *q, const void *k, const void *v, void *out, float *lse,
+                                       const int32_t *cu_seqlens, int n_seq, int64_t total_frames, int heads,
+                                       int d_head, float softmax_scale, int64_t row_stride_qkv, int32_t *dev_status,
+                                       int flags, int64_t wait_limit_ns, void *stream)
+{
+    if (!lse && n_seq > 0 && total_frames > 0)
+        return NLE_ERR_INVALID_ARG;
+    return launch_varlen_attn(q, k, v, out, lse, cu_seqlens, n_seq, total_frames, heads, d_head, softmax_scale,
+                              row_stride_qkv, dev_status, flags, wait_limit_ns, stream);
 }
 
 extern "C" int nle_varlen_attn_fwd(const void *q, const void *k, const void *v, void *out,

@@ -49,6 +49,14 @@ class RopePlan(ctypes.Structure):
                                                         "interleaved")] + [("eps", _f32), ("rot_scale", _f32)]
 
 
+class AttnBwdArgs(ctypes.Structure):
+    """nle_attn_bwd_args."""
+    _fields_ = [(n, _vp) for n in ("q", "k", "v", "out", "dout", "lse", "dq", "dk", "dv", "cu_seqlens", "workspace",
+                                   "dev_status")] + \
+        [(n, _i64) for n in ("total_frames", "row_stride_qkv", "row_stride_dqkv", "wait_limit_ns")] + \
+        [(n, _int) for n in ("n_seq", "heads", "d_head", "flags")] + [("softmax_scale", _f32)]
+
+
 NLE_ROPE_BWD_WORKSPACE_BYTES = 1 << 20
 
 
@@ -74,6 +82,10 @@ _SIGS = {
     "nle_varlen_attn_fwd": ([_vp, _vp, _vp, _vp, _vp, _int, _i64, _int, _int, _vp], _int),
     "nle_varlen_attn_fwd_ex": ([_vp, _vp, _vp, _vp, _vp, _int, _i64, _int, _int, _f32, _i64, _vp, _int, _i64,
                                 _vp], _int),
+    "nle_block_attn_fwd_lse": ([_vp] * 6 + [_int, _i64, _int, _int, _int, _f32, _i64, _vp, _int, _i64, _vp], _int),
+    "nle_varlen_attn_fwd_lse": ([_vp] * 6 + [_int, _i64, _int, _int, _f32, _i64, _vp, _int, _i64, _vp], _int),
+    "nle_block_attn_bwd": ([ctypes.POINTER(AttnBwdArgs), _int, _vp], _int),
+    "nle_varlen_attn_bwd": ([ctypes.POINTER(AttnBwdArgs), _vp], _int),
     "nle_qk_norm_rope_fwd": ([ctypes.POINTER(RopePlan)] + [_vp, _i64] * 4 + [_vp], _int),
     "nle_qk_norm_rope_bwd": ([ctypes.POINTER(RopePlan)] + [_vp, _i64] * 6 + [_vp] * 4, _int),
     "nle_ctc_greedy_fwd": ([_vp, _i64, _int, _vp, _int, _i64, _vp, _vp, _vp, _vp], _int),
@@ -347,6 +359,8 @@ def _rows(t, name: str, frames: int | None = None, device=None):
         raise ValueError(f"{name}: [frames, heads, 64] required")
     if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != 64)):
         raise ValueError(f"{name}: dense heads of 64 required (only the frame stride may vary)")
+    if t.numel() and t.shape[0] > 1 and t.stride(0) < t.shape[1] * 64:
+        raise ValueError(f"{name}: overlapping frames (an expanded tensor?)")
     if frames is not None and t.shape[0] != frames:
         raise ValueError(f"{name}: {frames} frames required")
     if device is not None and t.device != device:
@@ -465,6 +479,111 @@ def qk_norm_rope_bwd(dq_out, dk_out, cu_seqlens, inv_freq, q=None, k=None, q_wei
                                          x_strides[1], _ptr(dq), strides[2], _ptr(dk), strides[3], _ptr(dw_q),
                                          _ptr(dw_k), _ptr(work), sid), "nle_qk_norm_rope_bwd")
     return dq, dk, dw_q, dw_k
+
+
+# ------------------------------------------------------------------ training forms of the attentions
+def _qkv_rows(q, k, v):
+    """Checks q, k, v ([frames, heads, 64], one shape and frame stride);
+    returns their frame stride (0: dense)."""
+    stride = _rows(q, "q")
+    for t, n in ((k, "k"), (v, "v")):
+        if t.shape != q.shape:
+            raise ValueError(f"{n}: the shape of q required")
+        if _rows(t, n, None, q.device) != stride:
+            raise ValueError(f"{n}: the frame stride of q required")
+    return stride
+
+
+def _cu_on(cu_seqlens, device, dev_status=None):
+    for t, n in ((cu_seqlens, "cu_seqlens"), (dev_status, "dev_status")):
+        if t is not None:
+            _dev_tensor(t, n, torch.int32)
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1 or not cu_seqlens.is_contiguous():
+        raise ValueError("cu_seqlens: contiguous [n_seq + 1] required")
+    _on(device, cu_seqlens=cu_seqlens, dev_status=dev_status)
+
+
+def _attn_lse(q, k, v, cu_seqlens, block_frames, softmax_scale, out, dev_status, flags, wait_limit_ns, stream):
+    stride = _qkv_rows(q, k, v)
+    _cu_on(cu_seqlens, q.device, dev_status)
+    frames, heads = q.shape[0], q.shape[1]
+    with _Scope(q.device, stream) as sid:
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        else:
+            _rows(out, "out", frames, q.device)
+            if out.shape != q.shape or not out.is_contiguous():
+                raise ValueError("out: contiguous, of the shape of q, required")
+        lse = torch.empty((heads, frames), dtype=torch.float32, device=q.device)
+        head = (_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(cu_seqlens), cu_seqlens.numel() - 1, frames,
+                heads, 64)
+        tail = (float(softmax_scale), stride, _ptr(dev_status), flags, wait_limit_ns, sid)
+        if block_frames is None:
+            _check(_lib.nle_varlen_attn_fwd_lse(*head, *tail), "nle_varlen_attn_fwd_lse")
+        else:
+            _check(_lib.nle_block_attn_fwd_lse(*head, block_frames, *tail), "nle_block_attn_fwd_lse")
+    return out, lse
+
+
+def block_attn_lse(q, k, v, cu_seqlens, block_frames: int = 200, softmax_scale: float = 0.0, out=None,
+                   dev_status=None, flags: int = 0, wait_limit_ns: int = 0, stream=None):
+    """(out, lse) of block attention: the output of :func:`block_attn` and what
+    :func:`block_attn_bwd` needs of it, lse float32 [heads, frames].  q, k and
+    v may be views of one projection buffer (a common frame stride)."""
+    return _attn_lse(q, k, v, cu_seqlens, block_frames, softmax_scale, out, dev_status, flags, wait_limit_ns, stream)
+
+
+def varlen_attn_lse(q, k, v, cu_seqlens, softmax_scale: float = 0.0, out=None, dev_status=None, flags: int = 0,
+                    wait_limit_ns: int = 0, stream=None):
+    """(out, lse) of full attention inside each utterance, as :func:`block_attn_lse`."""
+    return _attn_lse(q, k, v, cu_seqlens, None, softmax_scale, out, dev_status, flags, wait_limit_ns, stream)
+
+
+def _attn_bwd(dout, q, k, v, out, lse, cu_seqlens, block_frames, softmax_scale, grads, dev_status, flags,
+              wait_limit_ns, stream):
+    stride = _qkv_rows(q, k, v)
+    frames, heads = q.shape[0], q.shape[1]
+    for t, n in ((dout, "dout"), (out, "out")):
+        _dev_tensor(t, n, torch.bfloat16)
+        if t.shape != q.shape or not t.is_contiguous():
+            raise ValueError(f"{n}: contiguous, of the shape of q, required")
+    _dev_tensor(lse, "lse", torch.float32)
+    if lse.shape != (heads, frames) or not lse.is_contiguous():
+        raise ValueError(f"lse: contiguous [{heads}, {frames}] required")
+    _cu_on(cu_seqlens, q.device, dev_status)
+    _on(q.device, dout=dout, out=out, lse=lse)
+    with _Scope(q.device, stream) as sid:
+        strides = []
+        dq, dk, dv = _outputs(grads, (q, k, v), ("dq", "dk", "dv"), strides)
+        if strides[1] != strides[0] or strides[2] != strides[0]:
+            raise ValueError("dq, dk and dv: one frame stride required")
+        work = torch.empty(max(frames * heads, 1), dtype=torch.float32, device=q.device)
+        args = AttnBwdArgs(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(dout), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv),
+                           _ptr(cu_seqlens), _ptr(work), _ptr(dev_status), frames, stride, strides[0], wait_limit_ns,
+                           cu_seqlens.numel() - 1, heads, 64, flags, float(softmax_scale))
+        if block_frames is None:
+            _check(_lib.nle_varlen_attn_bwd(ctypes.byref(args), sid), "nle_varlen_attn_bwd")
+        else:
+            _check(_lib.nle_block_attn_bwd(ctypes.byref(args), block_frames, sid), "nle_block_attn_bwd")
+    return dq, dk, dv
+
+
+def block_attn_bwd(dout, q, k, v, out, lse, cu_seqlens, block_frames: int = 200, softmax_scale: float = 0.0,
+                   grads=None, dev_status=None, flags: int = 0, wait_limit_ns: int = 0, stream=None):
+    """(dq, dk, dv) of block attention from the gradient ``dout`` of its output,
+    its inputs, and (out, lse) of :func:`block_attn_lse` with the same
+    block_frames and softmax_scale.  ``grads``: (dq, dk, dv) to write, which
+    may be views of one buffer; frames of no utterance are not written (new
+    tensors hold anything there)."""
+    return _attn_bwd(dout, q, k, v, out, lse, cu_seqlens, block_frames, softmax_scale, grads, dev_status, flags,
+                     wait_limit_ns, stream)
+
+
+def varlen_attn_bwd(dout, q, k, v, out, lse, cu_seqlens, softmax_scale: float = 0.0, grads=None, dev_status=None,
+                    flags: int = 0, wait_limit_ns: int = 0, stream=None):
+    """(dq, dk, dv) of full attention inside each utterance, as :func:`block_attn_bwd`."""
+    return _attn_bwd(dout, q, k, v, out, lse, cu_seqlens, None, softmax_scale, grads, dev_status, flags,
+                     wait_limit_ns, stream)
 
 
 # ------------------------------------------------------------------ windowed cross-attention

@@ -228,6 +228,68 @@ int nle_varlen_attn_fwd_ex(const void *q, const void *k, const void *v, void *ou
                            int64_t wait_limit_ns, void *stream);
 
 /* ---------------------------------------------------------------------
+ * Training forms of block attention and of full-utterance attention: the
+ * forward pass that also keeps every row's log-sum-exp, and the gradient.
+ *
+ * nle_*_fwd_lse: as the _ex form (the same out, bit for bit), plus
+ * lse  device float [heads][total_frames], out:
+ *      lse[h][i] = ln sum_j exp(softmax_scale * q_i.k_j) over the frames j
+ *      that frame i attends to (natural log); 4-byte aligned.  Entries of
+ *      frames of no utterance are not written.
+ *
+ * nle_*_bwd: with P_ij = exp(s q_i.k_j - lse_i), s = softmax_scale, and
+ * delta_i = sum_d dout_id out_id, all sums over the block (utterance):
+ *     dV_j = sum_i P_ij dO_i,   dS_ij = P_ij (dO_i.v_j - delta_i),
+ *     dQ_i = s sum_j dS_ij k_j, dK_j = s sum_i dS_ij q_i.
+ * Products accumulate in fp32; P and dS are rounded once to bf16 before the
+ * products that take them (a relative 2^-8 at most for each term), and the
+ * gradients once to bf16.  No atomics: the same bits on every call.
+ *
+ * nle_attn_bwd_args (host struct, device pointers):
+ *   q, k, v      bf16, as the forward's, frames row_stride_qkv elements
+ *                apart (0: heads * 64; a multiple of 8)
+ *   out, dout    bf16 [total_frames][heads][64], dense: the forward's output
+ *                and its gradient
+ *   lse          float [heads][total_frames], of the forward
+ *   dq, dk, dv   bf16, out: frames row_stride_dqkv elements apart (0:
+ *                heads * 64; a multiple of 8), so that they may lie inside
+ *                one fused gradient buffer; frames of no utterance are not
+ *                written.  They must not overlap any input.
+ *   workspace    4 * heads * total_frames bytes of device scratch, 16-byte
+ *                aligned, used by this call alone until it has run
+ *   cu_seqlens, n_seq, total_frames, heads, d_head, softmax_scale,
+ *   dev_status, flags, wait_limit_ns: as the forward's _ex form
+ * block_frames must be the forward's (1..256).  q, k, v, out, dout, dq, dk
+ * and dv are 16-byte aligned.  Two kernels on `stream`; no allocation.
+ * Errors as for the forward entry points.
+ */
+int nle_block_attn_fwd_lse(const void *q, const void *k, const void *v, void *out, float *lse,
+                           const int32_t *cu_seqlens, int n_seq, int64_t total_frames, int heads, int d_head,
+                           int block_frames, float softmax_scale, int64_t row_stride_qkv, int32_t *dev_status,
+                           int flags, int64_t wait_limit_ns, void *stream);
+
+int nle_varlen_attn_fwd_lse(const void *q, const void *k, const void *v, void *out, float *lse,
+                            const int32_t *cu_seqlens, int n_seq, int64_t total_frames, int heads, int d_head,
+                            float softmax_scale, int64_t row_stride_qkv, int32_t *dev_status, int flags,
+                            int64_t wait_limit_ns, void *stream);
+
+typedef struct {
+    const void *q, *k, *v, *out, *dout;
+    const float *lse;
+    void *dq, *dk, *dv;
+    const int32_t *cu_seqlens;
+    void *workspace;
+    int32_t *dev_status;
+    int64_t total_frames, row_stride_qkv, row_stride_dqkv, wait_limit_ns;
+    int n_seq, heads, d_head, flags;
+    float softmax_scale;
+} nle_attn_bwd_args;
+
+int nle_block_attn_bwd(const nle_attn_bwd_args *args, int block_frames, void *stream);
+
+int nle_varlen_attn_bwd(const nle_attn_bwd_args *args, void *stream);
+
+/* ---------------------------------------------------------------------
  * Per-head RMS norm of queries and keys and the rotary position rotation, in
  * one pass, and the gradient (the positions of the bidirectional editor's
  * attention; the rotated q and k are what nle_varlen_attn_fwd takes).
