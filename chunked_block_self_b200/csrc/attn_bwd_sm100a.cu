@@ -22,25 +22,28 @@
 // (query, key) pair instead of 5 and 1, which costs less than the fp32
 // atomics (32 KB per 128 x 128 tile) that a single pass would add.
 //
-// One persistent CTA per SM, 12 warps:
+// One persistent CTA per SM, 20 warps:
 //   warp 0   TMA producer: owner tiles (two stages), the segment's tiles into
 //            a ring; publishes every item's descriptor.
-//   warp 1   MMA issuer (one elected lane).  S and D of tile t + 1 are issued
-//            before the accumulating MMAs of tile t, so they run while the
-//            elementwise warps work on tile t.
+//   warp 1   issues S and D (one elected lane): S of tile t + 1 runs while the
+//            elementwise warps work on tile t, D as soon as they have read t's.
 //   warp 2   tile fix-up: zeroes tile rows past the segment (up to the MMA's
 //            16-row granule: their P is 0, but 0 * Inf would be NaN) and, for
 //            kind 0, stages the tile's lse and delta (+inf and 0 past the
 //            segment, so that P and dS vanish there).
-//   warp 3   owns TMEM.
-//   warps 4-11  elementwise, two warpgroups: every lane owns one row of the
-//            tile (its TMEM lane), warpgroup g the columns 64g..64g+63:
+//   warp 3   owns TMEM and issues the accumulating MMAs (one elected lane).
+//   warps 4-19  elementwise, four warpgroups: every lane owns one row of the
+//            tile (its TMEM lane), warpgroup g the columns 32g..32g+31:
 //            P = exp2(S s log2e - lse log2e), dS = P (D - delta) in fp32, both
 //            rounded once to bf16 (the A operands of the accumulating MMAs)
 //            and written over S; then the output rows (acc times s, rounded
 //            to bf16, 16-byte stores of the segment's rows only).
+// The code of one tile is one short straight line per kind: the first form
+// (two warpgroups, 64 columns each, unrolled: about 40 KB of code walked per
+// tile) missed the instruction cache on 27 % of its requests, and the MMA
+// warp, idle in between, paid for each miss (4.2 k cycles a tile).
 // TMEM (512 columns): S buffers at 0 and 128 (after use: warpgroup g's P in
-// columns 64g..64g+31, its dS in 64g+32..64g+63), D at 256, acc0 at 384,
+// columns 32g..32g+15, its dS in 32g+16..32g+31), D at 256, acc0 at 384,
 // acc1 at 448.
 //
 // Every mbarrier wait is bounded; on expiry the CTA drains its copies and
@@ -55,17 +58,22 @@ namespace {
 
 using namespace nle;
 
-constexpr int kThreads = 384;
 constexpr int kElem0 = 4;                            // first elementwise warp
-constexpr int kElemWarps = 8;
+constexpr int kElemWarps = 16;                       // four warpgroups
+constexpr int kThreads = 32 * (kElem0 + kElemWarps); // 640
+constexpr int kCols = 32;                            // tile columns of a warpgroup
 constexpr int kRows = 128;                           // owner rows, and rows of a tile
 constexpr int kRowBytes = 128;                       // one frame of one head: 64 bf16
 constexpr uint32_t kMatBytes = kRows * kRowBytes;    // 16 KB
 constexpr uint32_t kPairBytes = 2 * kMatBytes;       // X, Y (owner) or x, y (tile)
-constexpr uint32_t kColBytes = 2 * kRows * 4;        // a tile's lse (log2 domain) and delta
-constexpr int kMaxRing = 5;
+constexpr uint32_t kColBytes = 2 * kRows * 4;        // a tile's -lse (log2 domain) and -delta
+constexpr uint32_t kRing = 4;                        // tiles in flight
 constexpr int kDescRing = 4;
-constexpr int kDescReaders = 2 + kElemWarps;         // MMA, fix-up and elementwise warps
+constexpr int kDescReaders = 3 + kElemWarps;         // both MMA, fix-up and elementwise warps
+// shared memory: two owner stages, the tile ring, the tiles' columns, the barriers
+constexpr uint32_t kRingOff = 2 * kPairBytes;
+constexpr uint32_t kColOff = kRingOff + kRing * kPairBytes;
+constexpr uint32_t kBarsOff = kColOff + kRing * kColBytes;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kDCol = 256, kAcc0 = 384, kAcc1 = 448;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -80,16 +88,16 @@ struct ItemDesc {
 struct Bars {
     uint64_t own_full[2];
     uint64_t own_empty[2];          // the item's last S and D MMAs have completed
-    uint64_t t_full[kMaxRing];
-    uint64_t t_ready[kMaxRing];     // the fix-up warp has checked the tile
-    uint64_t t_empty[kMaxRing];     // the tile's accumulating MMAs have completed
+    uint64_t t_full[kRing];
+    uint64_t t_ready[kRing];     // the fix-up warp has checked the tile
+    uint64_t t_empty[kRing];     // the tile's accumulating MMAs have completed
     uint64_t s_full[2];
     uint64_t s_empty[2];            // the accumulating MMAs that read P, dS have completed
     uint64_t d_full;
     uint64_t d_empty;               // kElemWarps arrivals: D has been read
     uint64_t p_full[2];             // kElemWarps arrivals: P and dS written
     uint64_t acc_full;              // the item's accumulators are complete
-    uint64_t mma_done;
+    uint64_t mma_done[2];
     uint64_t desc_full[kDescRing];
     uint64_t desc_empty[kDescRing]; // kDescReaders arrivals
     ItemDesc desc[kDescRing];
@@ -104,8 +112,6 @@ struct Params {
     int heads;
     int block;          // frames per segment; 0: whole utterances
     int xtiles;         // owner tiles per block (block mode)
-    int ring;
-    uint32_t ring_off, col_off, bars_off;
     float scale, scale_log2;
     const float *lse;   // [heads][total]
     const float *delta; // [heads][total]
@@ -191,133 +197,155 @@ struct DescReader {
     }
 };
 
-// The tiles of an item that lie ahead of the MMA warp's accumulating side.
-struct Cursor {
-    ItemDesc d;
-    int tiles, j;   // tiles of the item; the current one
-};
-
-// 32 columns of the tile for this lane's row: P (in place of S's values).
-__device__ __forceinline__ void probs(float (&s)[64], int c0, float sl2, float row_lse2, const float *col_lse2,
-                                      bool by_col)
+// ---------------------------------------------------------------- packed fp32 pairs
+__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi)
 {
-    if (by_col) {
-#pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-            const float4 l = *reinterpret_cast<const float4 *>(col_lse2 + c0 + i);
-            s[c0 + i] = ex2_approx(fmaf(s[c0 + i], sl2, -l.x));
-            s[c0 + i + 1] = ex2_approx(fmaf(s[c0 + i + 1], sl2, -l.y));
-            s[c0 + i + 2] = ex2_approx(fmaf(s[c0 + i + 2], sl2, -l.z));
-            s[c0 + i + 3] = ex2_approx(fmaf(s[c0 + i + 3], sl2, -l.w));
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            s[c0 + i] = ex2_approx(fmaf(s[c0 + i], sl2, -row_lse2));
-    }
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+    return r;
 }
 
-// One tile for one lane: P and dS of the warpgroup's 64 columns.  nc: columns
-// of the MMA extent that lie in the warpgroup's half (a multiple of 16, > 0);
-// valid: columns inside the segment (kind 1 masks the others by index).
+__device__ __forceinline__ uint64_t pair(float lo, float hi)
+{
+    return pair(__float_as_uint(lo), __float_as_uint(hi));
+}
+
+__device__ __forceinline__ void unpair(uint64_t p, float &lo, float &hi)
+{
+    uint32_t a, b;
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(p));
+    lo = __uint_as_float(a);
+    hi = __uint_as_float(b);
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// One tile for one lane: P and dS of the warpgroup's 32 columns, written over
+// its columns of S (P, kind 0 only, over the first 16, dS over the rest).
+// neg_lse2, neg_delta: -lse log2e and -delta, of the lane's row (kind 1) or,
+// from shared memory, of the columns (kind 0).  valid: columns inside the
+// segment; kind 1 masks the others by index (kind 0's have lse = +inf, so
+// P = 0, and zeroed operands, so D = 0).  False if the wait for D ran out.
 template <bool kDQ>
-__device__ __forceinline__ bool elem_tile(uint32_t tS, uint32_t tD, int nc, int valid, float sl2, float row_lse2,
-                                          float row_delta, const float *col_lse2, const float *col_delta, Bars *bars,
+__device__ __forceinline__ bool elem_tile(uint32_t tS, uint32_t tD, int valid, float sl2, float neg_lse2,
+                                          float neg_delta, const float *col_lse2, const float *col_delta, Bars *bars,
                                           uint32_t d_parity, const Params &p, volatile int *abort_flag)
 {
-    const int lane = threadIdx.x & 31;
-    float s[64];
-    uint32_t *su = reinterpret_cast<uint32_t *>(s);
-    const bool two = nc > 32;   // warp-uniform
-    tmem_ld32_nowait(tS, su);
-    if (two)
-        tmem_ld32_nowait(tS + 32, su + 32);
+    uint32_t s[kCols], d[kCols], pk[kCols / 2];
+    tmem_ld32_nowait(tS, s);
     tmem_wait_ld();
 #pragma unroll
-    for (int i = 0; i < 64; ++i)
-        reg_fence(su[i]);
+    for (int i = 0; i < kCols; ++i)
+        reg_fence(s[i]);
+    const uint64_t k2 = pair(sl2, sl2);
+    uint64_t pr[kCols / 2];
 #pragma unroll
-    for (int c0 = 0; c0 < 64; c0 += 32) {
-        if (c0 && !two)
-            break;
-        probs(s, c0, sl2, row_lse2, col_lse2, !kDQ);
-        if (kDQ && valid < c0 + 32) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                s[c0 + i] = c0 + i < valid ? s[c0 + i] : 0.f;
+    for (int i = 0; i < kCols / 4; ++i) {
+        uint64_t l0, l1;
+        if (kDQ) {
+            l0 = l1 = pair(neg_lse2, neg_lse2);
+        } else {
+            const float4 l = reinterpret_cast<const float4 *>(col_lse2)[i];
+            l0 = pair(l.x, l.y);
+            l1 = pair(l.z, l.w);
         }
-        if (!kDQ) {
-            uint32_t pk[16];
+        const uint64_t y0 = fma2(pair(s[4 * i], s[4 * i + 1]), k2, l0);
+        const uint64_t y1 = fma2(pair(s[4 * i + 2], s[4 * i + 3]), k2, l1);
+        float a, b;
+        unpair(y0, a, b);
+        pr[2 * i] = pair(ex2_approx(a), ex2_approx(b));
+        unpair(y1, a, b);
+        pr[2 * i + 1] = pair(ex2_approx(a), ex2_approx(b));
+    }
+    if (!kDQ) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                pk[i] = pack_bf16x2(s[c0 + 2 * i], s[c0 + 2 * i + 1]);
-            tmem_st16p(tS + c0 / 2, pk);
+        for (int i = 0; i < kCols / 2; ++i) {
+            float a, b;
+            unpair(pr[i], a, b);
+            pk[i] = pack_bf16x2(a, b);
         }
+        tmem_st16p(tS, pk);
     }
     if (!wait_bar(smem_u32(&bars->d_full), d_parity, abort_flag, p.wait_ns, p.status))
         return false;
     tc_fence_after();
+    tmem_ld32_nowait(tD, d);
+    tmem_wait_ld();
 #pragma unroll
-    for (int c0 = 0; c0 < 64; c0 += 32) {
-        if (c0 && !two)
-            break;
-        uint32_t d[32], pk[16];
-        tmem_ld32_nowait(tD + c0, d);
-        tmem_wait_ld();
+    for (int i = 0; i < kCols; ++i)
+        reg_fence(d[i]);
+    tc_fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0)
+        mbar_arrive(smem_u32(&bars->d_empty));
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            reg_fence(d[i]);
-        if (c0 == 32 || !two) {   // D has been read
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(smem_u32(&bars->d_empty));
-        }
+    for (int i = 0; i < kCols / 4; ++i) {
+        uint64_t l0, l1;
         if (kDQ) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                // masked places: P is 0, but D may be anything
-                const float x = s[c0 + i] * (__uint_as_float(d[i]) - row_delta);
-                s[c0 + i] = valid < c0 + 32 && c0 + i >= valid ? 0.f : x;
-            }
+            l0 = l1 = pair(neg_delta, neg_delta);
         } else {
-#pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-                const float4 dl = *reinterpret_cast<const float4 *>(col_delta + c0 + i);
-                s[c0 + i] *= __uint_as_float(d[i]) - dl.x;
-                s[c0 + i + 1] *= __uint_as_float(d[i + 1]) - dl.y;
-                s[c0 + i + 2] *= __uint_as_float(d[i + 2]) - dl.z;
-                s[c0 + i + 3] *= __uint_as_float(d[i + 3]) - dl.w;
-            }
+            const float4 l = reinterpret_cast<const float4 *>(col_delta)[i];
+            l0 = pair(l.x, l.y);
+            l1 = pair(l.z, l.w);
         }
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            pk[i] = pack_bf16x2(s[c0 + 2 * i], s[c0 + 2 * i + 1]);
-        tmem_st16p(tS + 32 + c0 / 2, pk);
+        pr[2 * i] = mul2(pr[2 * i], add2(pair(d[4 * i], d[4 * i + 1]), l0));
+        pr[2 * i + 1] = mul2(pr[2 * i + 1], add2(pair(d[4 * i + 2], d[4 * i + 3]), l1));
     }
+    if (kDQ && valid < kCols) {   // warp-uniform: the segment's last tile
+#pragma unroll
+        for (int i = 0; i < kCols / 2; ++i) {
+            float a, b;
+            unpair(pr[i], a, b);
+            pr[i] = pair(2 * i < valid ? a : 0.f, 2 * i + 1 < valid ? b : 0.f);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kCols / 2; ++i) {
+        float a, b;
+        unpair(pr[i], a, b);
+        pk[i] = pack_bf16x2(a, b);
+    }
+    tmem_st16p(tS + kCols / 2, pk);
     tmem_wait_st();
     return true;
 }
 
-// `cols` columns of an accumulator row, times f, to bf16 at dst.
-__device__ __forceinline__ void store_acc(uint32_t tacc, int cols, float f, __nv_bfloat16 *dst, bool row_ok)
+// 32 columns of an accumulator row, times f, to bf16 at dst.
+__device__ __forceinline__ void store_acc(uint32_t tacc, float f, __nv_bfloat16 *dst, bool row_ok)
 {
-    for (int c = 0; c < cols; c += 32) {
-        uint32_t o[32];
-        tmem_ld32_nowait(tacc + c, o);
-        tmem_wait_ld();
+    uint32_t o[32];
+    tmem_ld32_nowait(tacc, o);
+    tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            reg_fence(o[i]);
-        if (row_ok) {
+    for (int i = 0; i < 32; ++i)
+        reg_fence(o[i]);
+    if (row_ok) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 8)
-                *reinterpret_cast<uint4 *>(dst + c + i) =
-                    make_uint4(pack_bf16x2(__uint_as_float(o[i]) * f, __uint_as_float(o[i + 1]) * f),
-                               pack_bf16x2(__uint_as_float(o[i + 2]) * f, __uint_as_float(o[i + 3]) * f),
-                               pack_bf16x2(__uint_as_float(o[i + 4]) * f, __uint_as_float(o[i + 5]) * f),
-                               pack_bf16x2(__uint_as_float(o[i + 6]) * f, __uint_as_float(o[i + 7]) * f));
-        }
+        for (int i = 0; i < 32; i += 8)
+            *reinterpret_cast<uint4 *>(dst + i) =
+                make_uint4(pack_bf16x2(__uint_as_float(o[i]) * f, __uint_as_float(o[i + 1]) * f),
+                           pack_bf16x2(__uint_as_float(o[i + 2]) * f, __uint_as_float(o[i + 3]) * f),
+                           pack_bf16x2(__uint_as_float(o[i + 4]) * f, __uint_as_float(o[i + 5]) * f),
+                           pack_bf16x2(__uint_as_float(o[i + 6]) * f, __uint_as_float(o[i + 7]) * f));
     }
 }
 
@@ -329,12 +357,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t own_base = smem_u32(smem);
-    const uint32_t ring_base = own_base + p.ring_off;
-    float *cols = reinterpret_cast<float *>(smem + p.col_off);   // per stage: lse2[128], delta[128]
-    Bars *bars = reinterpret_cast<Bars *>(smem + p.bars_off);
+    const uint32_t ring_base = own_base + kRingOff;
+    float *cols = reinterpret_cast<float *>(smem + kColOff);   // per stage: -lse2[128], -delta[128]
+    Bars *bars = reinterpret_cast<Bars *>(smem + kBarsOff);
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const int ring = p.ring;
 
     // ------------------------------------------------------------ set-up
     if (threadIdx.x == 0) {
@@ -345,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&bars->s_empty[s]), 1);
             mbar_init(smem_u32(&bars->p_full[s]), kElemWarps);
         }
-        for (int s = 0; s < ring; ++s) {
+        for (int s = 0; s < (int)kRing; ++s) {
             mbar_init(smem_u32(&bars->t_full[s]), 1);
             mbar_init(smem_u32(&bars->t_ready[s]), 1);
             mbar_init(smem_u32(&bars->t_empty[s]), 1);
@@ -353,7 +380,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(smem_u32(&bars->d_full), 1);
         mbar_init(smem_u32(&bars->d_empty), kElemWarps);
         mbar_init(smem_u32(&bars->acc_full), 1);
-        mbar_init(smem_u32(&bars->mma_done), 1);
+        mbar_init(smem_u32(&bars->mma_done[0]), 1);
+        mbar_init(smem_u32(&bars->mma_done[1]), 1);
         for (int j = 0; j < kDescRing; ++j) {
             mbar_init(smem_u32(&bars->desc_full[j]), 1);
             mbar_init(smem_u32(&bars->desc_empty[j]), kDescReaders);
@@ -422,8 +450,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             ++nown;
             for (int j = 0; j * kRows < d.T; ++j) {
-                const int s = nt % ring;
-                const uint32_t u = (uint32_t)(nt / ring);
+                const int s = nt % (int)kRing;
+                const uint32_t u = (uint32_t)(nt / (int)kRing);
                 if (u > 0 && !wait_bar(smem_u32(&bars->t_empty[s]), (u - 1) & 1, abort_flag, wait_ns, p.status)) {
                     stop = true;
                     break;
@@ -448,131 +476,114 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int m = nown - 2; m < nown; ++m)
                 if (m >= 0 && !(skip0 && m == 0))
                     wait_bar_drain(smem_u32(&bars->own_full[m & 1]), (uint32_t)(m >> 1) & 1, wait_ns);
-            for (int m = nt - ring; m < nt; ++m)
+            for (int m = nt - (int)kRing; m < nt; ++m)
                 if (m >= 0)
-                    wait_bar_drain(smem_u32(&bars->t_full[m % ring]), (uint32_t)(m / ring) & 1, wait_ns);
+                    wait_bar_drain(smem_u32(&bars->t_full[m % (int)kRing]), (uint32_t)(m / (int)kRing) & 1, wait_ns);
         }
         __syncwarp();
     } else if (warp == 1) {
-        // ======================================================== MMA issuer
+        // ======================================================== S and D MMAs
         DescReader rd{0};
-        Cursor front{}, back{};
-        int tf = 0, tb = 0;  // tiles issued by the front (S, D) and the back (accumulators)
-        int nown = 0;        // items entered by the front
+        ItemDesc d;
+        uint32_t nt = 0, n = 0;
+        const uint64_t own0 = smem_desc_sw128(own_base, 16, 1024), ring0 = smem_desc_sw128(ring_base, 16, 1024);
         bool ok = true;
-        bool more = rd.next(bars, p, abort_flag, front.d);
-        const uint32_t id_acc = idesc_bf16_f32(128, 64, true);
-
-        auto enter = [&]() -> bool {   // the front's item: its owner tile must have landed
-            front.tiles = (front.d.T + kRows - 1) / kRows;
-            front.j = 0;
-            const int os = nown & 1;
-            return wait_bar(smem_u32(&bars->own_full[os]), (uint32_t)(nown >> 1) & 1, abort_flag, wait_ns, p.status);
-        };
-        auto front_issue = [&]() -> bool {   // S and D of the front's tile
-            const int s = tf % ring, b = tf & 1;
-            const uint32_t u = (uint32_t)tf >> 1;   // uses of S buffer b before this one
-            if (!wait_bar(smem_u32(&bars->t_ready[s]), (uint32_t)(tf / ring) & 1, abort_flag, wait_ns, p.status))
-                return false;
-            if (u > 0 && !wait_bar(smem_u32(&bars->s_empty[b]), (u - 1) & 1, abort_flag, wait_ns, p.status))
-                return false;
-            tc_fence_after();
-            const int nv = min(kRows, front.d.T - front.j * kRows);
-            const uint32_t id = idesc_bf16_f32(128, (nv + 15) & ~15, false);
-            const uint32_t xo = own_base + (nown & 1) * kPairBytes, xt = ring_base + s * kPairBytes;
-            {
-                const uint64_t da = smem_desc_sw128(xo, 16, 1024), db = smem_desc_sw128(xt, 16, 1024);
+        while (ok && rd.next(bars, p, abort_flag, d)) {
+            const uint32_t os = n & 1;
+            if (!wait_bar(smem_u32(&bars->own_full[os]), (n >> 1) & 1, abort_flag, wait_ns, p.status))
+                break;
+            const uint64_t da = own0 + os * (kPairBytes >> 4);
+            for (int left = __shfl_sync(kFull, d.T, 0); left > 0; left -= kRows, ++nt) {
+                const uint32_t s = nt % kRing, b = nt & 1;
+                if (!wait_bar(smem_u32(&bars->t_ready[s]), (nt / kRing) & 1, abort_flag, wait_ns, p.status) ||
+                    (nt >= 2 &&
+                     !wait_bar(smem_u32(&bars->s_empty[b]), ((nt >> 1) - 1) & 1, abort_flag, wait_ns, p.status))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint64_t db = ring0 + s * (kPairBytes >> 4);
+                const uint32_t id = idesc_bf16_f32(128, left < kRows ? (left + 15) & ~15 : kRows, false);
+                const uint32_t ts = tmem + b * 128;
+                // K steps of 16 elements = 32 bytes inside the 128-byte swizzle atom
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        mma_ss(tmem + b * 128, da + 2 * kk, db + 2 * kk, id, kk > 0 ? 1u : 0u);
+                        mma_ss(ts, da + 2 * kk, db + 2 * kk, id, kk > 0 ? 1u : 0u);
                     mma_commit(smem_u32(&bars->s_full[b]));
                 }
                 __syncwarp();
-            }
-            if (tf > 0 &&
-                !wait_bar(smem_u32(&bars->d_empty), (uint32_t)(tf - 1) & 1, abort_flag, wait_ns, p.status))
-                return false;
-            tc_fence_after();
-            {
-                const uint64_t da = smem_desc_sw128(xo + kMatBytes, 16, 1024),
-                               db = smem_desc_sw128(xt + kMatBytes, 16, 1024);
+                if (nt > 0 &&
+                    !wait_bar(smem_u32(&bars->d_empty), (nt - 1) & 1, abort_flag, wait_ns, p.status)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
                 if (elect_one()) {
+                    constexpr uint64_t kY = kMatBytes >> 4;   // from X, x to Y, y
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        mma_ss(tmem + kDCol, da + 2 * kk, db + 2 * kk, id, kk > 0 ? 1u : 0u);
+                        mma_ss(tmem + kDCol, da + kY + 2 * kk, db + kY + 2 * kk, id, kk > 0 ? 1u : 0u);
                     mma_commit(smem_u32(&bars->d_full));
-                    if (front.j == front.tiles - 1)   // the item's last use of its owner tile
-                        mma_commit(smem_u32(&bars->own_empty[nown & 1]));
+                    if (left <= kRows)   // the item's last use of its owner tile
+                        mma_commit(smem_u32(&bars->own_empty[os]));
                 }
                 __syncwarp();
             }
-            ++tf;
-            return true;
-        };
-        auto back_issue = [&]() -> bool {   // the accumulating MMAs of the back's tile
-            const int s = tb % ring, b = tb & 1;
-            if (!wait_bar(smem_u32(&bars->p_full[b]), ((uint32_t)tb >> 1) & 1, abort_flag, wait_ns, p.status))
-                return false;
-            tc_fence_after();
-            const int nv = min(kRows, back.d.T - back.j * kRows);
-            const int steps = (nv + 15) >> 4;
-            const uint32_t xt = ring_base + s * kPairBytes;
-            // N = 64 is one 128-byte swizzle atom along N; K steps of 16
-            // rows advance the start by 2048 bytes
-            const uint64_t dx = smem_desc_sw128(xt, 0, 1024), dy = smem_desc_sw128(xt + kMatBytes, 0, 1024);
-            if (elect_one()) {
-                const uint32_t sb = tmem + b * 128;
-                for (int kk = 0; kk < steps; ++kk) {
-                    const uint32_t a = sb + (kk >> 2) * 64 + (kk & 3) * 8;
-                    const uint32_t acc = back.j > 0 || kk > 0 ? 1u : 0u;
-                    const uint64_t row = (uint64_t)(kk * (16 * kRowBytes >> 4));
-                    if (back.d.kind == 0)
-                        mma_ts(tmem + kAcc1, a, dy + row, id_acc, acc);
-                    mma_ts(tmem + kAcc0, a + 32, dx + row, id_acc, acc);
-                }
-                mma_commit(smem_u32(&bars->t_empty[s]));
-                mma_commit(smem_u32(&bars->s_empty[b]));
-                if (back.j == back.tiles - 1)
-                    mma_commit(smem_u32(&bars->acc_full));
-            }
-            __syncwarp();
-            ++tb;
-            return true;
-        };
-
-        if (more) {
-            ok = enter() && front_issue();
-            back = front;
-            while (ok) {
-                // the front moves one tile on: the next of its item, or the next item's first
-                bool ahead = false;   // the front is at a tile that has been issued and the back has not reached
-                if (front.j + 1 < front.tiles) {
-                    ++front.j;
-                    ahead = true;
-                } else {
-                    ++nown;
-                    ahead = more = rd.next(bars, p, abort_flag, front.d);
-                    if (!more && *abort_flag) {
-                        ok = false;
-                        break;
-                    }
-                    if (more)
-                        ok = enter();
-                }
-                if (ok && ahead)
-                    ok = front_issue();
-                if (!ok || !back_issue())
-                    break;
-                if (!ahead)
-                    break;
-                back = front;
-            }
+            ++n;
         }
         // every MMA must finish before TMEM is released
         if (elect_one()) {
-            mma_commit(smem_u32(&bars->mma_done));
-            wait_bar_drain(smem_u32(&bars->mma_done), 0, wait_ns);
+            mma_commit(smem_u32(&bars->mma_done[0]));
+            wait_bar_drain(smem_u32(&bars->mma_done[0]), 0, wait_ns);
+        }
+        __syncwarp();
+    } else if (warp == 3) {
+        // ======================================================== accumulating MMAs
+        DescReader rd{0};
+        ItemDesc d;
+        uint32_t nt = 0;
+        const uint64_t ring0 = smem_desc_sw128(ring_base, 0, 1024);
+        const uint32_t id = idesc_bf16_f32(128, 64, true);
+        bool ok = true;
+        while (ok && rd.next(bars, p, abort_flag, d)) {
+            const bool both = __shfl_sync(kFull, d.kind, 0) == 0;
+            uint32_t acc = 0;
+            for (int left = __shfl_sync(kFull, d.T, 0); left > 0; left -= kRows, ++nt) {
+                const uint32_t s = nt % kRing, b = nt & 1;
+                if (!wait_bar(smem_u32(&bars->p_full[b]), (nt >> 1) & 1, abort_flag, wait_ns, p.status)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                // N = 64 is one 128-byte swizzle atom along N; K steps of 16
+                // rows advance the start by 2048 bytes
+                const uint64_t dx = ring0 + s * (kPairBytes >> 4), dy = dx + (kMatBytes >> 4);
+                const uint32_t a = tmem + b * 128;
+                const int steps = left < kRows ? (left + 15) >> 4 : kRows / 16;
+                if (elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < kRows / 16; ++kk) {
+                        if (kk < steps) {
+                            const uint32_t ak = a + (kk >> 1) * kCols + (kk & 1) * 8;
+                            const uint64_t row = (uint64_t)(kk * (16 * kRowBytes >> 4));
+                            if (both)
+                                mma_ts(tmem + kAcc1, ak, dy + row, id, kk ? 1u : acc);
+                            mma_ts(tmem + kAcc0, ak + kCols / 2, dx + row, id, kk ? 1u : acc);
+                        }
+                    }
+                    mma_commit(smem_u32(&bars->t_empty[s]));
+                    mma_commit(smem_u32(&bars->s_empty[b]));
+                    if (left <= kRows)
+                        mma_commit(smem_u32(&bars->acc_full));
+                }
+                __syncwarp();
+                acc = 1;
+            }
+        }
+        if (elect_one()) {
+            mma_commit(smem_u32(&bars->mma_done[1]));
+            wait_bar_drain(smem_u32(&bars->mma_done[1]), 0, wait_ns);
         }
         __syncwarp();
     } else if (warp == 2) {
@@ -583,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         while (ok && rd.next(bars, p, abort_flag, d)) {
             for (int j = 0; j * kRows < d.T; ++j, ++nt) {
-                const int s = nt % ring;
+                const int s = nt % (int)kRing;
                 const int nv = min(kRows, d.T - j * kRows);
                 const int nk = (nv + 15) & ~15;
                 float l[4], dl[4];
@@ -592,11 +603,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int c = lane + 32 * i;
-                        l[i] = c < nv ? __ldg(p.lse + at + c) * kLog2e : INFINITY;
-                        dl[i] = c < nv ? __ldg(p.delta + at + c) : 0.f;
+                        l[i] = c < nv ? __ldg(p.lse + at + c) * -kLog2e : -INFINITY;
+                        dl[i] = c < nv ? -__ldg(p.delta + at + c) : 0.f;
                     }
                 }
-                if (!wait_bar(smem_u32(&bars->t_full[s]), (uint32_t)(nt / ring) & 1, abort_flag, wait_ns, p.status)) {
+                if (!wait_bar(smem_u32(&bars->t_full[s]), (uint32_t)(nt / (int)kRing) & 1, abort_flag, wait_ns, p.status)) {
                     ok = false;
                     break;
                 }
@@ -610,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (nv < nk) {
                     for (int m = 0; m < 2; ++m) {
-                        uint4 *z = reinterpret_cast<uint4 *>(smem + p.ring_off + s * kPairBytes + m * kMatBytes +
+                        uint4 *z = reinterpret_cast<uint4 *>(smem + kRingOff + s * kPairBytes + m * kMatBytes +
                                                              nv * kRowBytes);
                         for (int i = lane; i < (nk - nv) * (kRowBytes / 16); i += 32)
                             z[i] = make_uint4(0, 0, 0, 0);
@@ -624,10 +635,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp >= kElem0) {
         // ======================================================== elementwise
-        const int g = (warp - kElem0) >> 2;   // warpgroup: columns 64g..64g+63
+        const int g = (warp - kElem0) >> 2;   // warpgroup: columns 32g..32g+31
         const int qq = warp & 3;              // TMEM lane quarter of this warp
         const uint32_t lanes = (uint32_t)(qq * 32) << 16;
-        const float sl2 = p.scale_log2;
         DescReader rd{0};
         ItemDesc d;
         int nt = 0, n = 0;
@@ -636,30 +646,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int row = qq * 32 + lane;
             const bool active = qq * 32 < d.rows;   // warp-uniform
             const bool row_ok = row < d.rows;
-            float row_lse2 = 0.f, row_delta = 0.f;
+            float neg_lse2 = 0.f, neg_delta = 0.f;
             if (d.kind == 1 && row_ok) {
                 const size_t at = (size_t)d.h * p.total + d.f0 + row;
-                row_lse2 = __ldg(p.lse + at) * kLog2e;
-                row_delta = __ldg(p.delta + at);
+                neg_lse2 = __ldg(p.lse + at) * -kLog2e;
+                neg_delta = -__ldg(p.delta + at);
             }
-            const int tiles = (d.T + kRows - 1) / kRows;
-            for (int j = 0; j < tiles; ++j, ++nt) {
-                const int b = nt & 1, s = nt % ring;
-                const int nv = min(kRows, d.T - j * kRows);
-                const int nc = ((nv + 15) & ~15) - 64 * g;   // MMA columns in this warpgroup's half
-                // the tile's lse and delta (kind 0) were staged before this
-                if (!wait_bar(smem_u32(&bars->t_ready[s]), (uint32_t)(nt / ring) & 1, abort_flag, wait_ns, p.status) ||
+            for (int left = d.T; left > 0; left -= kRows, ++nt) {
+                const int b = nt & 1, s = nt % (int)kRing;
+                const int valid = min(kRows, left) - kCols * g;   // columns of this warpgroup inside the segment
+                // kind 0: the tile's lse and delta were staged before t_ready
+                if ((d.kind == 0 && !wait_bar(smem_u32(&bars->t_ready[s]), (uint32_t)(nt / (int)kRing) & 1, abort_flag,
+                                              wait_ns, p.status)) ||
                     !wait_bar(smem_u32(&bars->s_full[b]), ((uint32_t)nt >> 1) & 1, abort_flag, wait_ns, p.status)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                if (active && nc > 0) {
-                    const uint32_t tS = tmem + b * 128 + 64 * g + lanes, tD = tmem + kDCol + 64 * g + lanes;
-                    const float *cl = cols + s * (2 * kRows) + 64 * g;
-                    ok = d.kind ? elem_tile<true>(tS, tD, nc, nv - 64 * g, sl2, row_lse2, row_delta, cl, cl + kRows,
+                if (active && valid > 0) {
+                    const uint32_t tS = tmem + b * 128 + kCols * g + lanes, tD = tmem + kDCol + kCols * g + lanes;
+                    const float *cl = cols + s * (2 * kRows) + kCols * g;
+                    ok = d.kind ? elem_tile<true>(tS, tD, valid, p.scale_log2, neg_lse2, neg_delta, cl, cl + kRows,
                                                   bars, (uint32_t)nt & 1, p, abort_flag)
-                                : elem_tile<false>(tS, tD, nc, nv - 64 * g, sl2, row_lse2, row_delta, cl, cl + kRows,
+                                : elem_tile<false>(tS, tD, valid, p.scale_log2, neg_lse2, neg_delta, cl, cl + kRows,
                                                    bars, (uint32_t)nt & 1, p, abort_flag);
                 } else {
                     ok = wait_bar(smem_u32(&bars->d_full), (uint32_t)nt & 1, abort_flag, wait_ns, p.status);
@@ -682,12 +691,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             if (active) {
                 const long long at = (long long)(d.f0 + row) * p.out_stride + d.h * 64;
-                if (d.kind)
-                    store_acc(tmem + kAcc0 + 32 * g + lanes, 32, p.scale, p.dq + at + 32 * g, row_ok);
-                else if (g == 0)
-                    store_acc(tmem + kAcc0 + lanes, 64, p.scale, p.dk + at, row_ok);
-                else
-                    store_acc(tmem + kAcc1 + lanes, 64, 1.f, p.dv + at, row_ok);
+                // kind 0: warpgroups 0, 1 store dK, 2, 3 dV; kind 1: 0, 1 store dQ
+                const int c = 32 * (g & 1);
+                if (d.kind == 0)
+                    store_acc(tmem + (g < 2 ? kAcc0 : kAcc1) + c + lanes, g < 2 ? p.scale : 1.f,
+                              (g < 2 ? p.dk : p.dv) + at + c, row_ok);
+                else if (g < 2)
+                    store_acc(tmem + kAcc0 + c + lanes, p.scale, p.dq + at + c, row_ok);
             }
             tc_fence_before();
         }
@@ -782,17 +792,10 @@ int launch_attn_bwd(const nle_attn_bwd_args *a, int block, void *stream)
     p.heads = a->heads;
     p.block = block;
     p.xtiles = xtiles;
-    const size_t bars_bytes = ((sizeof(Bars) + 127) / 128) * 128 + 1024;
-    int ring = (int)(((size_t)di.smem_optin - 2 * kPairBytes - bars_bytes) / (kPairBytes + kColBytes));
-    if (ring > kMaxRing)
-        ring = kMaxRing;
-    if (ring < 2)
+    // above half the SM's: one CTA per SM (it owns all TMEM)
+    const size_t smem = kBarsOff + ((sizeof(Bars) + 127) / 128) * 128 + 1024;
+    if (smem > (size_t)di.smem_optin)
         return NLE_ERR_UNSUPPORTED;
-    p.ring = ring;
-    p.ring_off = 2 * kPairBytes;
-    p.col_off = p.ring_off + (uint32_t)ring * kPairBytes;
-    p.bars_off = p.col_off + (uint32_t)ring * kColBytes;
-    const size_t smem = p.bars_off + bars_bytes;   // above half the SM's: one CTA per SM (it owns all TMEM)
     const double scale = a->softmax_scale > 0.f ? (double)a->softmax_scale : 1.0 / std::sqrt((double)a->d_head);
     p.scale = (float)scale;
     p.scale_log2 = (float)(scale * 1.4426950408889634);
