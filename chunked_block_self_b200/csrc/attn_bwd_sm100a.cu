@@ -59,26 +59,23 @@ namespace {
 using namespace nle;
 
 constexpr int kElem0 = 4;                            // first elementwise warp
-constexpr int kElemWarps = 16;                       // four groups of four, one per TMEM lane quarter
+constexpr int kElemWarps = 16;                       // four warpgroups
 constexpr int kThreads = 32 * (kElem0 + kElemWarps); // 640
-constexpr int kCols = 32;                            // tile columns of a group
-constexpr int kRows = 128;                           // owner rows
-constexpr int kTile = 64;                            // rows of a tile
+constexpr int kCols = 32;                            // tile columns of a warpgroup
+constexpr int kRows = 128;                           // owner rows, and rows of a tile
 constexpr int kRowBytes = 128;                       // one frame of one head: 64 bf16
-constexpr uint32_t kBoxBytes = kTile * kRowBytes;    // 8 KB: every TMA box is 64 frames
-constexpr uint32_t kMatBytes = kRows * kRowBytes;    // X or Y: 16 KB
-constexpr uint32_t kPairBytes = 2 * kMatBytes;       // X, Y
-constexpr uint32_t kStageBytes = 2 * kBoxBytes;      // x, y
-constexpr uint32_t kColBytes = 2 * kCols * 4;        // an elementwise warp's columns: -lse (log2 domain), -delta
-constexpr uint32_t kRing = 8;                        // tiles in flight
+constexpr uint32_t kMatBytes = kRows * kRowBytes;    // 16 KB
+constexpr uint32_t kPairBytes = 2 * kMatBytes;       // X, Y (owner) or x, y (tile)
+constexpr uint32_t kColBytes = 2 * kRows * 4;        // a tile's -lse (log2 domain) and -delta
+constexpr uint32_t kRing = 4;                        // tiles in flight
 constexpr int kDescRing = 4;
-constexpr int kDescReaders = 3 + kElemWarps;         // S, D, accumulating and elementwise warps
+constexpr int kDescReaders = 3 + kElemWarps;         // both MMA, fix-up and elementwise warps
 // shared memory: two owner stages, the tile ring, the tiles' columns, the barriers
 constexpr uint32_t kRingOff = 2 * kPairBytes;
-constexpr uint32_t kColOff = kRingOff + kRing * kStageBytes;
-constexpr uint32_t kBarsOff = kColOff + kElemWarps * kColBytes;
+constexpr uint32_t kColOff = kRingOff + kRing * kPairBytes;
+constexpr uint32_t kBarsOff = kColOff + kRing * kColBytes;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kStreamCols = 192, kDCol = 128, kAcc0 = 384, kAcc1 = 448;
+constexpr uint32_t kDCol = 256, kAcc0 = 384, kAcc1 = 448;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // One work item as the producer publishes it (rows < 0: no further item).
@@ -90,17 +87,17 @@ struct ItemDesc {
 
 struct Bars {
     uint64_t own_full[2];
-    uint64_t own_empty[2];          // 2 arrivals: the item's last S and last D MMA have completed
+    uint64_t own_empty[2];          // the item's last S and D MMAs have completed
     uint64_t t_full[kRing];
+    uint64_t t_ready[kRing];     // the fix-up warp has checked the tile
     uint64_t t_empty[kRing];     // the tile's accumulating MMAs have completed
-    uint64_t s_full[4];             // by tile & 3
-    uint64_t s_empty[4];            // the accumulating MMAs that read P, dS have completed
-    uint64_t p_full[4];             // kElemWarps / 2 arrivals: P and dS written
-    uint64_t d_full[2];             // by tile & 1
-    uint64_t d_empty[2];            // kElemWarps / 2 arrivals: D has been read
+    uint64_t s_full[2];
+    uint64_t s_empty[2];            // the accumulating MMAs that read P, dS have completed
+    uint64_t d_full;
+    uint64_t d_empty;               // kElemWarps arrivals: D has been read
+    uint64_t p_full[2];             // kElemWarps arrivals: P and dS written
     uint64_t acc_full;              // the item's accumulators are complete
-    uint64_t acc_empty;             // kElemWarps arrivals: they have been read
-    uint64_t mma_done[3];
+    uint64_t mma_done[2];
     uint64_t desc_full[kDescRing];
     uint64_t desc_empty[kDescRing]; // kDescReaders arrivals
     ItemDesc desc[kDescRing];
@@ -251,7 +248,7 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
 template <bool kDQ>
 __device__ __forceinline__ bool elem_tile(uint32_t tS, uint32_t tD, int valid, float sl2, float neg_lse2,
                                           float neg_delta, const float *col_lse2, const float *col_delta, Bars *bars,
-                                          int stream, uint32_t d_parity, const Params &p, volatile int *abort_flag)
+                                          uint32_t d_parity, const Params &p, volatile int *abort_flag)
 {
     uint32_t s[kCols], d[kCols], pk[kCols / 2];
     tmem_ld32_nowait(tS, s);
@@ -288,7 +285,7 @@ __device__ __forceinline__ bool elem_tile(uint32_t tS, uint32_t tD, int valid, f
         }
         tmem_st16p(tS, pk);
     }
-    if (!wait_bar(smem_u32(&bars->d_full[stream]), d_parity, abort_flag, p.wait_ns, p.status))
+    if (!wait_bar(smem_u32(&bars->d_full), d_parity, abort_flag, p.wait_ns, p.status))
         return false;
     tc_fence_after();
     tmem_ld32_nowait(tD, d);
@@ -299,7 +296,7 @@ __device__ __forceinline__ bool elem_tile(uint32_t tS, uint32_t tD, int valid, f
     tc_fence_before();
     __syncwarp();
     if ((threadIdx.x & 31) == 0)
-        mbar_arrive(smem_u32(&bars->d_empty[stream]));
+        mbar_arrive(smem_u32(&bars->d_empty));
 #pragma unroll
     for (int i = 0; i < kCols / 4; ++i) {
         uint64_t l0, l1;
@@ -361,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t own_base = smem_u32(smem);
     const uint32_t ring_base = own_base + kRingOff;
-    float *cols = reinterpret_cast<float *>(smem + kColOff);   // per elementwise warp: -lse2[32], -delta[32]
+    float *cols = reinterpret_cast<float *>(smem + kColOff);   // per stage: -lse2[128], -delta[128]
     Bars *bars = reinterpret_cast<Bars *>(smem + kBarsOff);
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -370,23 +367,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_u32(&bars->own_full[s]), 1);
-            mbar_init(smem_u32(&bars->own_empty[s]), 2);
-            mbar_init(smem_u32(&bars->d_full[s]), 1);
-            mbar_init(smem_u32(&bars->d_empty[s]), kElemWarps / 2);
-        }
-        for (int s = 0; s < 4; ++s) {
+            mbar_init(smem_u32(&bars->own_empty[s]), 1);
             mbar_init(smem_u32(&bars->s_full[s]), 1);
             mbar_init(smem_u32(&bars->s_empty[s]), 1);
-            mbar_init(smem_u32(&bars->p_full[s]), kElemWarps / 2);
+            mbar_init(smem_u32(&bars->p_full[s]), kElemWarps);
         }
         for (int s = 0; s < (int)kRing; ++s) {
             mbar_init(smem_u32(&bars->t_full[s]), 1);
+            mbar_init(smem_u32(&bars->t_ready[s]), 1);
             mbar_init(smem_u32(&bars->t_empty[s]), 1);
         }
+        mbar_init(smem_u32(&bars->d_full), 1);
+        mbar_init(smem_u32(&bars->d_empty), kElemWarps);
         mbar_init(smem_u32(&bars->acc_full), 1);
-        mbar_init(smem_u32(&bars->acc_empty), kElemWarps);
-        for (int s = 0; s < 3; ++s)
-            mbar_init(smem_u32(&bars->mma_done[s]), 1);
+        mbar_init(smem_u32(&bars->mma_done[0]), 1);
+        mbar_init(smem_u32(&bars->mma_done[1]), 1);
         for (int j = 0; j < kDescRing; ++j) {
             mbar_init(smem_u32(&bars->desc_full[j]), 1);
             mbar_init(smem_u32(&bars->desc_empty[j]), kDescReaders);
@@ -448,16 +443,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0 && !(skip0 && nown == 0)) {
                 const uint32_t bar = smem_u32(&bars->own_full[os]);
                 const uint32_t dst = own_base + os * kPairBytes;
-                const int boxes = d.rows > kTile ? 2 : 1;
-                mbar_arrive_expect_tx(bar, 2 * boxes * kBoxBytes);
-                for (int x = 0; x < boxes; ++x) {
-                    tma_load(dst + x * kBoxBytes, d.kind ? &tm_q : &tm_k, d.h * 64, d.f0 + x * kTile, bar);
-                    tma_load(dst + kMatBytes + x * kBoxBytes, d.kind ? &tm_do : &tm_v, d.h * 64, d.f0 + x * kTile, bar);
-                }
+                mbar_arrive_expect_tx(bar, kPairBytes);
+                tma_load(dst, d.kind ? &tm_q : &tm_k, d.h * 64, d.f0, bar);
+                tma_load(dst + kMatBytes, d.kind ? &tm_do : &tm_v, d.h * 64, d.f0, bar);
             }
             __syncwarp();
             ++nown;
-            for (int j = 0; j * kTile < d.T; ++j) {
+            for (int j = 0; j * kRows < d.T; ++j) {
                 const int s = nt % (int)kRing;
                 const uint32_t u = (uint32_t)(nt / (int)kRing);
                 if (u > 0 && !wait_bar(smem_u32(&bars->t_empty[s]), (u - 1) & 1, abort_flag, wait_ns, p.status)) {
@@ -466,10 +458,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (lane == 0) {
                     const uint32_t bar = smem_u32(&bars->t_full[s]);
-                    const uint32_t dst = ring_base + s * kStageBytes;
-                    mbar_arrive_expect_tx(bar, kStageBytes);
-                    tma_load(dst, d.kind ? &tm_k : &tm_q, d.h * 64, d.s0 + j * kTile, bar);
-                    tma_load(dst + kBoxBytes, d.kind ? &tm_v : &tm_do, d.h * 64, d.s0 + j * kTile, bar);
+                    const uint32_t dst = ring_base + s * kPairBytes;
+                    mbar_arrive_expect_tx(bar, kPairBytes);
+                    tma_load(dst, d.kind ? &tm_k : &tm_q, d.h * 64, d.s0 + j * kRows, bar);
+                    tma_load(dst + kMatBytes, d.kind ? &tm_v : &tm_do, d.h * 64, d.s0 + j * kRows, bar);
                 }
                 __syncwarp();
                 ++nt;
@@ -489,50 +481,51 @@ __global__ void __launch_bounds__(kThreads, 1)
                     wait_bar_drain(smem_u32(&bars->t_full[m % (int)kRing]), (uint32_t)(m / (int)kRing) & 1, wait_ns);
         }
         __syncwarp();
-    } else if (warp == 1 || warp == 2) {
-        // ======================================================== S (warp 1) and D (warp 2) MMAs
-        const bool is_d = warp == 2;
+    } else if (warp == 1) {
+        // ======================================================== S and D MMAs
         DescReader rd{0};
         ItemDesc d;
         uint32_t nt = 0, n = 0;
-        const uint64_t own0 = smem_desc_sw128(own_base + (is_d ? kMatBytes : 0), 16, 1024);
-        const uint64_t ring0 = smem_desc_sw128(ring_base + (is_d ? kBoxBytes : 0), 16, 1024);
-        const uint32_t sh = is_d ? 1 : 2;   // D has one buffer a stream (two in all), S two (four)
-        uint64_t *full = is_d ? bars->d_full : bars->s_full, *empty = is_d ? bars->d_empty : bars->s_empty;
+        const uint64_t own0 = smem_desc_sw128(own_base, 16, 1024), ring0 = smem_desc_sw128(ring_base, 16, 1024);
         bool ok = true;
         while (ok && rd.next(bars, p, abort_flag, d)) {
             const uint32_t os = n & 1;
             if (!wait_bar(smem_u32(&bars->own_full[os]), (n >> 1) & 1, abort_flag, wait_ns, p.status))
                 break;
             const uint64_t da = own0 + os * (kPairBytes >> 4);
-            for (int left = __shfl_sync(kFull, d.T, 0); left > 0; left -= kTile, ++nt) {
-                const uint32_t s = nt % kRing, b = nt & ((1u << sh) - 1), u = nt >> sh;
-                if (!wait_bar(smem_u32(&bars->t_full[s]), (nt / kRing) & 1, abort_flag, wait_ns, p.status) ||
-                    (u > 0 && !wait_bar(smem_u32(&empty[b]), (u - 1) & 1, abort_flag, wait_ns, p.status))) {
+            for (int left = __shfl_sync(kFull, d.T, 0); left > 0; left -= kRows, ++nt) {
+                const uint32_t s = nt % kRing, b = nt & 1;
+                if (!wait_bar(smem_u32(&bars->t_ready[s]), (nt / kRing) & 1, abort_flag, wait_ns, p.status) ||
+                    (nt >= 2 &&
+                     !wait_bar(smem_u32(&bars->s_empty[b]), ((nt >> 1) - 1) & 1, abort_flag, wait_ns, p.status))) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                if (left < kTile && (left & 15)) {
-                    // rows past the segment up to the MMA's granule: their P
-                    // and dS are 0, but 0 * Inf would be NaN
-                    uint4 *z = reinterpret_cast<uint4 *>(smem + kRingOff + s * kStageBytes + (is_d ? kBoxBytes : 0) +
-                                                         left * kRowBytes);
-                    for (int i = lane; i < (16 - (left & 15)) * (kRowBytes / 16); i += 32)
-                        z[i] = make_uint4(0, 0, 0, 0);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
-                const uint64_t db = ring0 + s * (kStageBytes >> 4);
-                const uint32_t id = idesc_bf16_f32(128, left < kTile ? (left + 15) & ~15 : kTile, false);
-                const uint32_t t = tmem + (nt & 1) * kStreamCols + (is_d ? kDCol : ((nt >> 1) & 1) * kTile);
+                const uint64_t db = ring0 + s * (kPairBytes >> 4);
+                const uint32_t id = idesc_bf16_f32(128, left < kRows ? (left + 15) & ~15 : kRows, false);
+                const uint32_t ts = tmem + b * 128;
                 // K steps of 16 elements = 32 bytes inside the 128-byte swizzle atom
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        mma_ss(t, da + 2 * kk, db + 2 * kk, id, kk > 0 ? 1u : 0u);
-                    mma_commit(smem_u32(&full[b]));
-                    if (left <= kTile)   // the item's last use of its owner matrix
+                        mma_ss(ts, da + 2 * kk, db + 2 * kk, id, kk > 0 ? 1u : 0u);
+                    mma_commit(smem_u32(&bars->s_full[b]));
+                }
+                __syncwarp();
+                if (nt > 0 &&
+                    !wait_bar(smem_u32(&bars->d_empty), (nt - 1) & 1, abort_flag, wait_ns, p.status)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                if (elect_one()) {
+                    constexpr uint64_t kY = kMatBytes >> 4;   // from X, x to Y, y
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_ss(tmem + kDCol, da + kY + 2 * kk, db + kY + 2 * kk, id, kk > 0 ? 1u : 0u);
+                    mma_commit(smem_u32(&bars->d_full));
+                    if (left <= kRows)   // the item's last use of its owner tile
                         mma_commit(smem_u32(&bars->own_empty[os]));
                 }
                 __syncwarp();
@@ -541,41 +534,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // every MMA must finish before TMEM is released
         if (elect_one()) {
-            mma_commit(smem_u32(&bars->mma_done[is_d]));
-            wait_bar_drain(smem_u32(&bars->mma_done[is_d]), 0, wait_ns);
+            mma_commit(smem_u32(&bars->mma_done[0]));
+            wait_bar_drain(smem_u32(&bars->mma_done[0]), 0, wait_ns);
         }
         __syncwarp();
     } else if (warp == 3) {
         // ======================================================== accumulating MMAs
         DescReader rd{0};
         ItemDesc d;
-        uint32_t nt = 0, n = 0;
+        uint32_t nt = 0;
         const uint64_t ring0 = smem_desc_sw128(ring_base, 0, 1024);
-        constexpr uint32_t id = idesc_bf16_f32(128, 64, true);
+        const uint32_t id = idesc_bf16_f32(128, 64, true);
         bool ok = true;
         while (ok && rd.next(bars, p, abort_flag, d)) {
             const bool both = __shfl_sync(kFull, d.kind, 0) == 0;
             uint32_t acc = 0;
-            // p_full of a tile speaks for one stream's warps only: the other's
-            // may still be reading the last item's accumulators
-            if (n > 0 && !wait_bar(smem_u32(&bars->acc_empty), (n - 1) & 1, abort_flag, wait_ns, p.status))
-                break;
-            ++n;
-            for (int left = __shfl_sync(kFull, d.T, 0); left > 0; left -= kTile, ++nt) {
-                const uint32_t s = nt % kRing, b = nt & 3;
-                if (!wait_bar(smem_u32(&bars->p_full[b]), (nt >> 2) & 1, abort_flag, wait_ns, p.status)) {
+            for (int left = __shfl_sync(kFull, d.T, 0); left > 0; left -= kRows, ++nt) {
+                const uint32_t s = nt % kRing, b = nt & 1;
+                if (!wait_bar(smem_u32(&bars->p_full[b]), (nt >> 1) & 1, abort_flag, wait_ns, p.status)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 // N = 64 is one 128-byte swizzle atom along N; K steps of 16
                 // rows advance the start by 2048 bytes
-                const uint64_t dx = ring0 + s * (kStageBytes >> 4), dy = dx + (kBoxBytes >> 4);
-                const uint32_t a = tmem + (nt & 1) * kStreamCols + ((nt >> 1) & 1) * kTile;
-                const int steps = left < kTile ? (left + 15) >> 4 : kTile / 16;
+                const uint64_t dx = ring0 + s * (kPairBytes >> 4), dy = dx + (kMatBytes >> 4);
+                const uint32_t a = tmem + b * 128;
+                const int steps = left < kRows ? (left + 15) >> 4 : kRows / 16;
                 if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < kTile / 16; ++kk) {
+                    for (int kk = 0; kk < kRows / 16; ++kk) {
                         if (kk < steps) {
                             const uint32_t ak = a + (kk >> 1) * kCols + (kk & 1) * 8;
                             const uint64_t row = (uint64_t)(kk * (16 * kRowBytes >> 4));
@@ -584,9 +572,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                             mma_ts(tmem + kAcc0, ak + kCols / 2, dx + row, id, kk ? 1u : acc);
                         }
                     }
-                    mma_commit(smem_u32(&bars->s_empty[b]));
                     mma_commit(smem_u32(&bars->t_empty[s]));
-                    if (left <= kTile)
+                    mma_commit(smem_u32(&bars->s_empty[b]));
+                    if (left <= kRows)
                         mma_commit(smem_u32(&bars->acc_full));
                 }
                 __syncwarp();
@@ -594,69 +582,99 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         if (elect_one()) {
-            mma_commit(smem_u32(&bars->mma_done[2]));
-            wait_bar_drain(smem_u32(&bars->mma_done[2]), 0, wait_ns);
+            mma_commit(smem_u32(&bars->mma_done[1]));
+            wait_bar_drain(smem_u32(&bars->mma_done[1]), 0, wait_ns);
         }
         __syncwarp();
+    } else if (warp == 2) {
+        // ======================================================== tile fix-up
+        DescReader rd{0};
+        ItemDesc d;
+        int nt = 0;
+        bool ok = true;
+        while (ok && rd.next(bars, p, abort_flag, d)) {
+            for (int j = 0; j * kRows < d.T; ++j, ++nt) {
+                const int s = nt % (int)kRing;
+                const int nv = min(kRows, d.T - j * kRows);
+                const int nk = (nv + 15) & ~15;
+                float l[4], dl[4];
+                if (d.kind == 0) {
+                    const size_t at = (size_t)d.h * p.total + d.s0 + j * kRows;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int c = lane + 32 * i;
+                        l[i] = c < nv ? __ldg(p.lse + at + c) * -kLog2e : -INFINITY;
+                        dl[i] = c < nv ? -__ldg(p.delta + at + c) : 0.f;
+                    }
+                }
+                if (!wait_bar(smem_u32(&bars->t_full[s]), (uint32_t)(nt / (int)kRing) & 1, abort_flag, wait_ns, p.status)) {
+                    ok = false;
+                    break;
+                }
+                if (d.kind == 0) {
+                    float *cl = cols + s * (2 * kRows);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        cl[lane + 32 * i] = l[i];
+                        cl[kRows + lane + 32 * i] = dl[i];
+                    }
+                }
+                if (nv < nk) {
+                    for (int m = 0; m < 2; ++m) {
+                        uint4 *z = reinterpret_cast<uint4 *>(smem + kRingOff + s * kPairBytes + m * kMatBytes +
+                                                             nv * kRowBytes);
+                        for (int i = lane; i < (nk - nv) * (kRowBytes / 16); i += 32)
+                            z[i] = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_u32(&bars->t_ready[s]));
+            }
+        }
     } else if (warp >= kElem0) {
         // ======================================================== elementwise
-        const int g = (warp - kElem0) >> 2;   // group: stream g >> 1, columns 32 (g & 1) .. + 31
-        const int stream = g >> 1, c0 = kCols * (g & 1);
+        const int g = (warp - kElem0) >> 2;   // warpgroup: columns 32g..32g+31
         const int qq = warp & 3;              // TMEM lane quarter of this warp
         const uint32_t lanes = (uint32_t)(qq * 32) << 16;
-        const uint32_t tstream = tmem + stream * kStreamCols + c0 + lanes;
-        const int row = qq * 32 + lane;
-        float *cl = cols + (warp - kElem0) * (2 * kCols);
         DescReader rd{0};
-        // lse and delta of an item: of this lane's row (kind 1), or of the
-        // lane's column in tile j (kind 0; nothing past the segment: P = 0)
-        auto fetch = [&](const ItemDesc &d, int j, float &l, float &dl) {
-            const int c = j * kTile + c0 + lane;
-            const bool in = d.kind ? row < d.rows : c < d.T;
-            const size_t at = (size_t)d.h * p.total + (d.kind ? d.f0 + row : d.s0 + c);
-            l = in ? __ldg(p.lse + at) : d.kind ? 0.f : INFINITY;
-            dl = in ? __ldg(p.delta + at) : 0.f;
-        };
-        ItemDesc d, dn;
-        int nt0 = 0, n = 0;   // the item's first tile; items
-        float vl = 0.f, vd = 0.f;
-        bool ok = rd.next(bars, p, abort_flag, d);
-        if (ok)
-            fetch(d, stream, vl, vd);
-        for (; ok; ++n) {
+        ItemDesc d;
+        int nt = 0, n = 0;
+        bool ok = true;
+        for (; ok && rd.next(bars, p, abort_flag, d); ++n) {
+            const int row = qq * 32 + lane;
             const bool active = qq * 32 < d.rows;   // warp-uniform
-            const int tiles = (d.T + kTile - 1) / kTile;
-            const float neg_lse2 = vl * -kLog2e, neg_delta = -vd;   // kind 1
-            // the stream's tiles of the item
-            for (int j = (nt0 ^ stream) & 1; j < tiles; j += 2) {
-                const int nt = nt0 + j, b = nt & 3;
-                const int valid = min(kTile, d.T - j * kTile) - c0;   // columns of this group in the segment
-                const uint32_t dpar = (uint32_t)(nt >> 1) & 1;
-                if (d.kind == 0) {
-                    // the columns' values, for the whole warp
-                    __syncwarp();
-                    cl[lane] = vl * -kLog2e;
-                    cl[kCols + lane] = -vd;
-                    __syncwarp();
-                    if (j + 2 < tiles)
-                        fetch(d, j + 2, vl, vd);
-                }
-                if (!wait_bar(smem_u32(&bars->s_full[b]), ((uint32_t)nt >> 2) & 1, abort_flag, wait_ns, p.status)) {
+            const bool row_ok = row < d.rows;
+            float neg_lse2 = 0.f, neg_delta = 0.f;
+            if (d.kind == 1 && row_ok) {
+                const size_t at = (size_t)d.h * p.total + d.f0 + row;
+                neg_lse2 = __ldg(p.lse + at) * -kLog2e;
+                neg_delta = -__ldg(p.delta + at);
+            }
+            for (int left = d.T; left > 0; left -= kRows, ++nt) {
+                const int b = nt & 1, s = nt % (int)kRing;
+                const int valid = min(kRows, left) - kCols * g;   // columns of this warpgroup inside the segment
+                // kind 0: the tile's lse and delta were staged before t_ready
+                if ((d.kind == 0 && !wait_bar(smem_u32(&bars->t_ready[s]), (uint32_t)(nt / (int)kRing) & 1, abort_flag,
+                                              wait_ns, p.status)) ||
+                    !wait_bar(smem_u32(&bars->s_full[b]), ((uint32_t)nt >> 1) & 1, abort_flag, wait_ns, p.status)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 if (active && valid > 0) {
-                    const uint32_t tS = tstream + ((nt >> 1) & 1) * kTile, tD = tstream + kDCol;
-                    ok = d.kind ? elem_tile<true>(tS, tD, valid, p.scale_log2, neg_lse2, neg_delta, cl, cl + kCols,
-                                                  bars, stream, dpar, p, abort_flag)
-                                : elem_tile<false>(tS, tD, valid, p.scale_log2, neg_lse2, neg_delta, cl, cl + kCols,
-                                                   bars, stream, dpar, p, abort_flag);
+                    const uint32_t tS = tmem + b * 128 + kCols * g + lanes, tD = tmem + kDCol + kCols * g + lanes;
+                    const float *cl = cols + s * (2 * kRows) + kCols * g;
+                    ok = d.kind ? elem_tile<true>(tS, tD, valid, p.scale_log2, neg_lse2, neg_delta, cl, cl + kRows,
+                                                  bars, (uint32_t)nt & 1, p, abort_flag)
+                                : elem_tile<false>(tS, tD, valid, p.scale_log2, neg_lse2, neg_delta, cl, cl + kRows,
+                                                   bars, (uint32_t)nt & 1, p, abort_flag);
                 } else {
-                    ok = wait_bar(smem_u32(&bars->d_full[stream]), dpar, abort_flag, wait_ns, p.status);
+                    ok = wait_bar(smem_u32(&bars->d_full), (uint32_t)nt & 1, abort_flag, wait_ns, p.status);
                     __syncwarp();
                     if (lane == 0)
-                        mbar_arrive(smem_u32(&bars->d_empty[stream]));
+                        mbar_arrive(smem_u32(&bars->d_empty));
                 }
                 if (!ok)
                     break;
@@ -667,17 +685,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok)
                 break;
-            nt0 += tiles;
-            // the next item's values travel while this one's output is stored
-            const bool have = rd.next(bars, p, abort_flag, dn);
-            if (have)
-                fetch(dn, (nt0 ^ stream) & 1, vl, vd);
             // ---------------------------------------------- output rows
             if (!wait_bar(smem_u32(&bars->acc_full), (uint32_t)n & 1, abort_flag, wait_ns, p.status))
                 break;
             tc_fence_after();
             if (active) {
-                const bool row_ok = row < d.rows;
                 const long long at = (long long)(d.f0 + row) * p.out_stride + d.h * 64;
                 // kind 0: warpgroups 0, 1 store dK, 2, 3 dV; kind 1: 0, 1 store dQ
                 const int c = 32 * (g & 1);
@@ -688,11 +700,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     store_acc(tmem + kAcc0 + c + lanes, p.scale, p.dq + at + c, row_ok);
             }
             tc_fence_before();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(smem_u32(&bars->acc_empty));
-            d = dn;
-            ok = have;
         }
     }
 
@@ -775,7 +782,7 @@ int launch_attn_bwd(const nle_attn_bwd_args *a, int block, void *stream)
     // an even grid: the two kinds of an owner tile are taken in the same round
     const int grid = (int)(items < (di.sm_count & ~1) ? items : (di.sm_count & ~1));
     // the kernel counts the tiles that a CTA walks in 32 bits
-    if ((items / grid + 1) * ((block ? block : a->total_frames) / kTile + 1) > 0x7fffffffLL)
+    if ((items / grid + 1) * ((block ? block : a->total_frames) / kRows + 1) > 0x7fffffffLL)
         return NLE_ERR_UNSUPPORTED;
 
     Params p{};
@@ -804,10 +811,10 @@ int launch_attn_bwd(const nle_attn_bwd_args *a, int block, void *stream)
 
     CUtensorMap tq, tk, tv, tdo;
     const uint64_t cols = (uint64_t)dense, rows = (uint64_t)a->total_frames;
-    if (!nle::encode_tmap_bf16_2d(&tq, a->q, cols, rows, stride, 64, kTile) ||
-        !nle::encode_tmap_bf16_2d(&tk, a->k, cols, rows, stride, 64, kTile) ||
-        !nle::encode_tmap_bf16_2d(&tv, a->v, cols, rows, stride, 64, kTile) ||
-        !nle::encode_tmap_bf16_2d(&tdo, a->dout, cols, rows, dense, 64, kTile))
+    if (!nle::encode_tmap_bf16_2d(&tq, a->q, cols, rows, stride, 64, kRows) ||
+        !nle::encode_tmap_bf16_2d(&tk, a->k, cols, rows, stride, 64, kRows) ||
+        !nle::encode_tmap_bf16_2d(&tv, a->v, cols, rows, stride, 64, kRows) ||
+        !nle::encode_tmap_bf16_2d(&tdo, a->dout, cols, rows, dense, 64, kRows))
         return NLE_ERR_CUDA;
     if (!nle::allow_max_dynamic_smem(reinterpret_cast<const void *>(attn_bwd_kernel), dev, di.smem_optin))
         return NLE_ERR_CUDA;

@@ -146,25 +146,33 @@ def _dev_tensor(t, name, dtype):
         raise TypeError(f"{name} must be {dtype}")
 
 
-class _Scope:
-    """The device and stream that a call allocates and launches on: ``device``'s
-    current stream, or the one given.  What is allocated inside belongs to that
-    stream, so its memory cannot still be in use by work on another one."""
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
-    def __init__(self, device, stream):
-        self.ctx = None
+
+class _Scope:
+    """The device and stream that a call allocates and launches on: the device
+    of index ``index``, its current stream or the one given.  What is allocated
+    inside belongs to that stream, so its memory cannot still be in use by work
+    on another one.  ``with _Scope(...) as handle``."""
+    __slots__ = ("index", "ctx")
+
+    def __init__(self, index: int, stream):
+        self.index, self.ctx = index, None
         if stream is not None:
             if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(int(stream), device) if int(stream) else \
-                    torch.cuda.default_stream(device)
+                stream = torch.cuda.ExternalStream(int(stream), index) if int(stream) else \
+                    torch.cuda.default_stream(index)
+            if stream.device_index != index:
+                raise ValueError(f"stream: of device {stream.device_index}, the tensors on device {index}")
             self.ctx = torch.cuda.stream(stream)
-        elif device.index != torch.cuda.current_device():
-            self.ctx = torch.cuda.device(device)
+        elif index != torch.cuda.current_device():
+            self.ctx = torch.cuda.device(index)
 
-    def __enter__(self):
+    def __enter__(self) -> int:
         if self.ctx is not None:
             self.ctx.__enter__()
-        return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(self.index)
 
     def __exit__(self, *exc):
         if self.ctx is not None:
@@ -351,72 +359,77 @@ def rope_inv_freq(rot_dim: int = 64, base: float = 10000.0, device="cuda", *, li
     return torch.from_numpy(f).to(device), scale
 
 
-def _rows(t, name: str, frames: int | None = None, device=None):
+def _rows(t, name: str, frames: int | None = None, index: int | None = None) -> int:
     """Checks a bf16 [frames, heads, 64] CUDA tensor whose heads are dense
-    (frames may be strided); returns its row stride."""
-    _dev_tensor(t, name, torch.bfloat16)
-    if t.dim() != 3 or t.shape[2] != 64:
+    (frames may be strided); returns its row stride (0: dense)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16")
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != 64:
         raise ValueError(f"{name}: [frames, heads, 64] required")
-    if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != 64)):
-        raise ValueError(f"{name}: dense heads of 64 required (only the frame stride may vary)")
-    if t.numel() and t.shape[0] > 1 and t.stride(0) < t.shape[1] * 64:
-        raise ValueError(f"{name}: overlapping frames (an expanded tensor?)")
-    if frames is not None and t.shape[0] != frames:
+    if frames is not None and shape[0] != frames:
         raise ValueError(f"{name}: {frames} frames required")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name}: on {t.device}, the other tensors on {device}")
-    return t.stride(0) if t.shape[0] > 1 else 0
+    if index is not None and t.get_device() != index:
+        raise ValueError(f"{name}: on {t.device}, the other tensors on device {index}")
+    if t.is_contiguous():
+        return 0
+    rows, heads, elems = t.stride()
+    if elems != 1 or (shape[1] > 1 and heads != 64):
+        raise ValueError(f"{name}: dense heads of 64 required (only the frame stride may vary)")
+    if shape[0] <= 1:
+        return 0
+    if rows < shape[1] * 64:
+        raise ValueError(f"{name}: overlapping frames (an expanded tensor?)")
+    return rows
 
 
-def _on(device, **tensors):
-    """Every given tensor lies on ``device``."""
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name}: on {t.device}, the other tensors on {device}")
+def _small(t, name: str, dtype, numel: int, index: int) -> None:
+    """Checks an optional contiguous CUDA tensor of `numel` elements (-1: any)."""
+    if t is None:
+        return
+    _dev_tensor(t, name, dtype)
+    if not t.is_contiguous() or (numel >= 0 and t.numel() != numel):
+        raise ValueError(f"{name}: contiguous tensor" + (f" of {numel} elements" if numel >= 0 else "") + " required")
+    if t.get_device() != index:
+        raise ValueError(f"{name}: on {t.device}, the other tensors on device {index}")
 
 
-def _rope_plan(ref, q_heads, k_heads, cu_seqlens, inv_freq, q_weight, k_weight, eps, interleaved, rot_scale, positions,
-               dev_status):
-    """nle_rope_plan of checked tensors; ``ref``: a [frames, heads, 64] tensor."""
-    frames, dev = ref.shape[0], ref.device
+def _n_seq(cu_seqlens, index: int) -> int:
+    _small(cu_seqlens, "cu_seqlens", torch.int32, -1, index)
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens: [n_seq + 1] required")
+    return cu_seqlens.numel() - 1
+
+
+def _rope_plan(frames, index, q_heads, k_heads, cu_seqlens, inv_freq, q_weight, k_weight, eps, interleaved, rot_scale,
+               positions, dev_status):
+    """nle_rope_plan of checked tensors."""
     if cu_seqlens is None and positions is None:
         raise ValueError("cu_seqlens or positions is required")
-    for t, n, dt in ((cu_seqlens, "cu_seqlens", torch.int32), (positions, "positions", torch.int32),
-                     (q_weight, "q_weight", torch.bfloat16), (k_weight, "k_weight", torch.bfloat16),
-                     (inv_freq, "inv_freq", torch.float64), (dev_status, "dev_status", torch.int32)):
-        if t is not None:
-            _dev_tensor(t, n, dt)
-            if not t.is_contiguous():
-                raise ValueError(f"{n}: contiguous tensor required")
-    _on(dev, cu_seqlens=cu_seqlens, positions=positions, q_weight=q_weight, k_weight=k_weight, inv_freq=inv_freq,
-        dev_status=dev_status)
-    if cu_seqlens is not None and cu_seqlens.numel() < 1:
-        raise ValueError("cu_seqlens: [n_seq + 1] required")
-    if positions is not None and positions.numel() != frames:
-        raise ValueError(f"positions: [{frames}] required")
-    for t, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if t is not None and t.numel() != 64:
-            raise ValueError(f"{n}: [64] required")
-    rot_dim = 0 if inv_freq is None else 2 * inv_freq.numel()
+    n_seq = 0 if cu_seqlens is None else _n_seq(cu_seqlens, index)
+    _small(positions, "positions", torch.int32, frames, index)
+    _small(q_weight, "q_weight", torch.bfloat16, 64, index)
+    _small(k_weight, "k_weight", torch.bfloat16, 64, index)
+    _small(inv_freq, "inv_freq", torch.float64, -1, index)
+    _small(dev_status, "dev_status", torch.int32, -1, index)
     return RopePlan(_ptr(cu_seqlens), _ptr(positions), _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq),
-                    _ptr(dev_status), frames, 0 if cu_seqlens is None else cu_seqlens.numel() - 1, q_heads, k_heads, 64,
-                    rot_dim, int(interleaved), float(eps), float(rot_scale))
+                    _ptr(dev_status), frames, n_seq, q_heads, k_heads, 64,
+                    0 if inv_freq is None else 2 * inv_freq.numel(), int(interleaved), eps, rot_scale)
 
 
-def _outputs(out, like, names, strides):
+def _outputs(out, like, names, strides, index):
     """The tensors to write: those of ``out``, checked, or new dense ones; their
     row strides are appended to ``strides``."""
     if out is None:
         strides += [0] * len(like)
-        return [None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in like]
+        return [None if t is None else torch.empty_like(t, memory_format=torch.contiguous_format) for t in like]
     if len(out) != len(like):
         raise ValueError(f"out: {', '.join(names)} required")
     for o, t, n in zip(out, like, names):
-        if t is None:
-            strides.append(0)
-            continue
-        strides.append(_rows(o, n, t.shape[0], t.device))
-        if o.shape != t.shape:
+        strides.append(0 if t is None else _rows(o, n, t.shape[0], index))
+        if t is not None and o.shape != t.shape:
             raise ValueError(f"{n}: shape {tuple(t.shape)} required")
     return out
 
@@ -432,14 +445,19 @@ def qk_norm_rope(q, k, cu_seqlens, inv_freq, q_weight=None, k_weight=None, eps: 
     ref = q if q is not None else k
     if ref is None:
         raise ValueError("q or k is required")
-    strides = []
-    for t, n in ((q, "q"), (k, "k")):
-        strides.append(0 if t is None else _rows(t, n, ref.shape[0], ref.device))
-    plan = _rope_plan(ref, 0 if q is None else q.shape[1], 0 if k is None else k.shape[1], cu_seqlens, inv_freq,
-                      q_weight, k_weight, eps, interleaved, rot_scale, positions, dev_status)
-    with _Scope(ref.device, stream) as sid:
-        q_out, k_out = _outputs(out, (q, k), ("q_out", "k_out"), strides)
-        _check(_lib.nle_qk_norm_rope_fwd(ctypes.byref(plan), _ptr(q), strides[0], _ptr(k), strides[1], _ptr(q_out),
+    strides = [0, 0]
+    frames = index = None
+    if q is not None:
+        strides[0] = _rows(q, "q")
+        frames, index = q.shape[0], q.get_device()
+    if k is not None:
+        strides[1] = _rows(k, "k", frames, index)
+        frames, index = k.shape[0], k.get_device()
+    plan = _rope_plan(frames, index, 0 if q is None else q.shape[1], 0 if k is None else k.shape[1], cu_seqlens,
+                      inv_freq, q_weight, k_weight, eps, interleaved, rot_scale, positions, dev_status)
+    with _Scope(index, stream) as sid:
+        q_out, k_out = _outputs(out, (q, k), ("q_out", "k_out"), strides, index)
+        _check(_lib.nle_qk_norm_rope_fwd(plan, _ptr(q), strides[0], _ptr(k), strides[1], _ptr(q_out),
                                          strides[2], _ptr(k_out), strides[3], sid), "nle_qk_norm_rope_fwd")
     return q_out, k_out
 
@@ -456,25 +474,30 @@ def qk_norm_rope_bwd(dq_out, dk_out, cu_seqlens, inv_freq, q=None, k=None, q_wei
         raise ValueError("dq_out or dk_out is required")
     norm = q_weight is not None or k_weight is not None
     strides, x_strides = [], []
+    frames = index = None
     for d, x, w, n in ((dq_out, q, q_weight, "q"), (dk_out, k, k_weight, "k")):
-        strides.append(0 if d is None else _rows(d, f"d{n}_out", ref.shape[0], ref.device))
+        strides.append(0)
         x_strides.append(0)
-        if d is not None and norm:
+        if d is None:
+            continue
+        strides[-1] = _rows(d, f"d{n}_out", frames, index)
+        frames, index = d.shape[0], d.get_device()
+        if norm:
             if x is None or w is None:
                 raise ValueError(f"{n} and {n}_weight are required for the gradient of the norm")
-            x_strides[-1] = _rows(x, n, ref.shape[0], ref.device)
+            x_strides[-1] = _rows(x, n, frames, index)
             if x.shape != d.shape:
                 raise ValueError(f"d{n}_out and {n}: one shape required")
-    plan = _rope_plan(ref, 0 if dq_out is None else dq_out.shape[1], 0 if dk_out is None else dk_out.shape[1],
+    plan = _rope_plan(frames, index, 0 if dq_out is None else dq_out.shape[1], 0 if dk_out is None else dk_out.shape[1],
                       cu_seqlens, inv_freq, q_weight, k_weight, eps, interleaved, rot_scale, positions, dev_status)
-    with _Scope(ref.device, stream) as sid:
-        dq, dk = _outputs(out, (dq_out, dk_out), ("dq", "dk"), strides)
+    with _Scope(index, stream) as sid:
+        dq, dk = _outputs(out, (dq_out, dk_out), ("dq", "dk"), strides, index)
         dw_q = dw_k = work = None
         if norm:
             dw_q = None if dq_out is None else torch.empty(64, dtype=torch.float32, device=ref.device)
             dw_k = None if dk_out is None else torch.empty(64, dtype=torch.float32, device=ref.device)
             work = torch.empty(NLE_ROPE_BWD_WORKSPACE_BYTES, dtype=torch.uint8, device=ref.device)
-        _check(_lib.nle_qk_norm_rope_bwd(ctypes.byref(plan), _ptr(dq_out), strides[0], _ptr(dk_out), strides[1],
+        _check(_lib.nle_qk_norm_rope_bwd(plan, _ptr(dq_out), strides[0], _ptr(dk_out), strides[1],
                                          _ptr(q) if norm else None, x_strides[0], _ptr(k) if norm else None,
                                          x_strides[1], _ptr(dq), strides[2], _ptr(dk), strides[3], _ptr(dw_q),
                                          _ptr(dw_k), _ptr(work), sid), "nle_qk_norm_rope_bwd")
@@ -484,40 +507,35 @@ def qk_norm_rope_bwd(dq_out, dk_out, cu_seqlens, inv_freq, q=None, k=None, q_wei
 # ------------------------------------------------------------------ training forms of the attentions
 def _qkv_rows(q, k, v):
     """Checks q, k, v ([frames, heads, 64], one shape and frame stride);
-    returns their frame stride (0: dense)."""
+    returns their frame stride (0: dense), shape and device index."""
     stride = _rows(q, "q")
+    shape, index = q.shape, q.get_device()
     for t, n in ((k, "k"), (v, "v")):
-        if t.shape != q.shape:
-            raise ValueError(f"{n}: the shape of q required")
-        if _rows(t, n, None, q.device) != stride:
+        if _rows(t, n, None, index) != stride:
             raise ValueError(f"{n}: the frame stride of q required")
-    return stride
+        if t.shape != shape:
+            raise ValueError(f"{n}: the shape of q required")
+    return stride, shape, index
 
 
-def _cu_on(cu_seqlens, device, dev_status=None):
-    for t, n in ((cu_seqlens, "cu_seqlens"), (dev_status, "dev_status")):
-        if t is not None:
-            _dev_tensor(t, n, torch.int32)
-    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1 or not cu_seqlens.is_contiguous():
-        raise ValueError("cu_seqlens: contiguous [n_seq + 1] required")
-    _on(device, cu_seqlens=cu_seqlens, dev_status=dev_status)
+def _dense(t, name: str, shape, index: int) -> None:
+    if _rows(t, name, shape[0], index) or t.shape != shape:
+        raise ValueError(f"{name}: contiguous, of the shape of q, required")
 
 
 def _attn_lse(q, k, v, cu_seqlens, block_frames, softmax_scale, out, dev_status, flags, wait_limit_ns, stream):
-    stride = _qkv_rows(q, k, v)
-    _cu_on(cu_seqlens, q.device, dev_status)
-    frames, heads = q.shape[0], q.shape[1]
-    with _Scope(q.device, stream) as sid:
+    stride, shape, index = _qkv_rows(q, k, v)
+    n_seq = _n_seq(cu_seqlens, index)
+    _small(dev_status, "dev_status", torch.int32, -1, index)
+    frames, heads = shape[0], shape[1]
+    if out is not None:
+        _dense(out, "out", shape, index)
+    with _Scope(index, stream) as sid:
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        else:
-            _rows(out, "out", frames, q.device)
-            if out.shape != q.shape or not out.is_contiguous():
-                raise ValueError("out: contiguous, of the shape of q, required")
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
         lse = torch.empty((heads, frames), dtype=torch.float32, device=q.device)
-        head = (_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(cu_seqlens), cu_seqlens.numel() - 1, frames,
-                heads, 64)
-        tail = (float(softmax_scale), stride, _ptr(dev_status), flags, wait_limit_ns, sid)
+        head = (_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(cu_seqlens), n_seq, frames, heads, 64)
+        tail = (softmax_scale, stride, _ptr(dev_status), flags, wait_limit_ns, sid)
         if block_frames is None:
             _check(_lib.nle_varlen_attn_fwd_lse(*head, *tail), "nle_varlen_attn_fwd_lse")
         else:
@@ -541,30 +559,28 @@ def varlen_attn_lse(q, k, v, cu_seqlens, softmax_scale: float = 0.0, out=None, d
 
 def _attn_bwd(dout, q, k, v, out, lse, cu_seqlens, block_frames, softmax_scale, grads, dev_status, flags,
               wait_limit_ns, stream):
-    stride = _qkv_rows(q, k, v)
-    frames, heads = q.shape[0], q.shape[1]
-    for t, n in ((dout, "dout"), (out, "out")):
-        _dev_tensor(t, n, torch.bfloat16)
-        if t.shape != q.shape or not t.is_contiguous():
-            raise ValueError(f"{n}: contiguous, of the shape of q, required")
-    _dev_tensor(lse, "lse", torch.float32)
-    if lse.shape != (heads, frames) or not lse.is_contiguous():
-        raise ValueError(f"lse: contiguous [{heads}, {frames}] required")
-    _cu_on(cu_seqlens, q.device, dev_status)
-    _on(q.device, dout=dout, out=out, lse=lse)
-    with _Scope(q.device, stream) as sid:
+    stride, shape, index = _qkv_rows(q, k, v)
+    frames, heads = shape[0], shape[1]
+    _dense(dout, "dout", shape, index)
+    _dense(out, "out", shape, index)
+    _small(lse, "lse", torch.float32, heads * frames, index)
+    if lse.shape != (heads, frames):
+        raise ValueError(f"lse: [{heads}, {frames}] required")
+    n_seq = _n_seq(cu_seqlens, index)
+    _small(dev_status, "dev_status", torch.int32, -1, index)
+    with _Scope(index, stream) as sid:
         strides = []
-        dq, dk, dv = _outputs(grads, (q, k, v), ("dq", "dk", "dv"), strides)
+        dq, dk, dv = _outputs(grads, (q, k, v), ("dq", "dk", "dv"), strides, index)
         if strides[1] != strides[0] or strides[2] != strides[0]:
             raise ValueError("dq, dk and dv: one frame stride required")
-        work = torch.empty(max(frames * heads, 1), dtype=torch.float32, device=q.device)
+        work = torch.empty_like(lse)
         args = AttnBwdArgs(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(dout), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv),
                            _ptr(cu_seqlens), _ptr(work), _ptr(dev_status), frames, stride, strides[0], wait_limit_ns,
-                           cu_seqlens.numel() - 1, heads, 64, flags, float(softmax_scale))
+                           n_seq, heads, 64, flags, softmax_scale)
         if block_frames is None:
-            _check(_lib.nle_varlen_attn_bwd(ctypes.byref(args), sid), "nle_varlen_attn_bwd")
+            _check(_lib.nle_varlen_attn_bwd(args, sid), "nle_varlen_attn_bwd")
         else:
-            _check(_lib.nle_block_attn_bwd(ctypes.byref(args), block_frames, sid), "nle_block_attn_bwd")
+            _check(_lib.nle_block_attn_bwd(args, block_frames, sid), "nle_block_attn_bwd")
     return dq, dk, dv
 
 
