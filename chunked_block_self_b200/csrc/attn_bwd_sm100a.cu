@@ -50,6 +50,7 @@
 // MMAs in flight, frees TMEM and returns.
 #include <cmath>
 
+#include "attn_bwd.cuh"
 #include "nle.h"
 #include "nle_device.cuh"
 #include "nle_host.h"
@@ -76,7 +77,6 @@ constexpr uint32_t kColOff = kRingOff + kRing * kPairBytes;
 constexpr uint32_t kBarsOff = kColOff + kRing * kColBytes;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kDCol = 256, kAcc0 = 384, kAcc1 = 448;
-constexpr float kLog2e = 1.4426950408889634f;
 
 // One work item as the producer publishes it (rows < 0: no further item).
 struct ItemDesc {
@@ -121,14 +121,6 @@ struct Params {
     unsigned long long wait_ns;
     int flags;
 };
-
-__device__ __forceinline__ void tma_load(uint32_t dst, const void *tmap, int32_t x, int32_t y, uint32_t bar)
-{
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
-                 " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-                 "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar)
-                 : "memory");
-}
 
 // The CTA's items in order: item i = blockIdx.x + n * gridDim.x =
 // ((u * X + x) * H + h) * 2 + c; u = 128-row unit of an utterance (X = 1), or
@@ -196,48 +188,6 @@ struct DescReader {
         return d.rows >= 0;
     }
 };
-
-// ---------------------------------------------------------------- packed fp32 pairs
-__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi)
-{
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
-    return r;
-}
-
-__device__ __forceinline__ uint64_t pair(float lo, float hi)
-{
-    return pair(__float_as_uint(lo), __float_as_uint(hi));
-}
-
-__device__ __forceinline__ void unpair(uint64_t p, float &lo, float &hi)
-{
-    uint32_t a, b;
-    asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(p));
-    lo = __uint_as_float(a);
-    hi = __uint_as_float(b);
-}
-
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
-{
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
-{
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 
 // One tile for one lane: P and dS of the warpgroup's 32 columns, written over
 // its columns of S (P, kind 0 only, over the first 16, dS over the rest).
@@ -327,26 +277,6 @@ __device__ __forceinline__ bool elem_tile(uint32_t tS, uint32_t tD, int valid, f
     tmem_st16p(tS + kCols / 2, pk);
     tmem_wait_st();
     return true;
-}
-
-// 32 columns of an accumulator row, times f, to bf16 at dst.
-__device__ __forceinline__ void store_acc(uint32_t tacc, float f, __nv_bfloat16 *dst, bool row_ok)
-{
-    uint32_t o[32];
-    tmem_ld32_nowait(tacc, o);
-    tmem_wait_ld();
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-        reg_fence(o[i]);
-    if (row_ok) {
-#pragma unroll
-        for (int i = 0; i < 32; i += 8)
-            *reinterpret_cast<uint4 *>(dst + i) =
-                make_uint4(pack_bf16x2(__uint_as_float(o[i]) * f, __uint_as_float(o[i + 1]) * f),
-                           pack_bf16x2(__uint_as_float(o[i + 2]) * f, __uint_as_float(o[i + 3]) * f),
-                           pack_bf16x2(__uint_as_float(o[i + 4]) * f, __uint_as_float(o[i + 5]) * f),
-                           pack_bf16x2(__uint_as_float(o[i + 6]) * f, __uint_as_float(o[i + 7]) * f));
-    }
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -826,6 +756,32 @@ int launch_attn_bwd(const nle_attn_bwd_args *a, int block, void *stream)
         static_cast<float *>(a->workspace), p.total, a->heads);
     if (cudaGetLastError() != cudaSuccess)
         return NLE_ERR_CUDA;
+    const bool whole = block && !(a->flags & NLE_FLAG_SPLIT_ITEMS) && (a->flags & NLE_FLAG_WHOLE_ITEMS);
+    if (whole) {
+        nle::BlockBwdArgs b{};
+        b.q = a->q;
+        b.k = a->k;
+        b.v = a->v;
+        b.dout = a->dout;
+        b.lse = a->lse;
+        b.delta = p.delta;
+        b.dq = a->dq;
+        b.dk = a->dk;
+        b.dv = a->dv;
+        b.cu = a->cu_seqlens;
+        b.status = a->dev_status;
+        b.total = a->total_frames;
+        b.stride = stride;
+        b.dstride = dstride;
+        b.n_seq = a->n_seq;
+        b.heads = a->heads;
+        b.block = block;
+        b.scale = p.scale;
+        b.scale_log2 = p.scale_log2;
+        b.wait_ns = p.wait_ns;
+        b.flags = a->flags;
+        return nle::launch_block_bwd(b, di, dev, units * a->heads, st);
+    }
     attn_bwd_kernel<<<grid, kThreads, smem, st>>>(tq, tk, tv, tdo, p);
     return cudaGetLastError() == cudaSuccess ? NLE_OK : NLE_ERR_CUDA;
 }

@@ -73,16 +73,17 @@ def _check_grads(grads, x, out, segs, scale=0.125, rows=None):
                                tol[keep][bad][:4], want[keep][bad][:4])
 
 
+@pytest.mark.parametrize("flags", [2, 4])   # whole blocks, tiles
 @pytest.mark.parametrize("block", [1, 2, 15, 16, 17, 48, 63, 64, 65, 97, 127, 128, 129, 143, 192, 200, 208, 255, 256])
-def test_block_gradient(block, cuda_device):
+def test_block_gradient(block, flags, cuda_device):
     """Block lengths around every tile and MMA granule; utterances of one frame,
-    shorter than, equal to and just past whole blocks."""
+    shorter than, equal to and just past whole blocks; both work splits."""
     lengths = [1, block, 2 * block + 1, 0, max(1, block - 1), 3 * block + block // 2]
     x = _inputs(lengths, 3, 100 + block)
     out, lse = _fwd(x, block)
     segs = attn_bwd.segments(x["cu"], block)
     _check_lse(lse, x, segs)
-    _check_grads(_bwd(x, block, out, lse), x, out, segs)
+    _check_grads(_bwd(x, block, out, lse, flags=flags), x, out, segs)
 
 
 @pytest.mark.parametrize("lengths", [
