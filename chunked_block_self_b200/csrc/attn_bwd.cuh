@@ -17,6 +17,20 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const void *tmap, int32_t
                  : "memory");
 }
 
+// Register split between the warpgroups of a 640-thread CTA launched with 96
+// registers a thread (61,440): the service warpgroup keeps 64, each of the
+// four elementwise ones takes 104 (8,192 + 53,248 = 61,440).  Executed by
+// every warp of the warpgroup.
+__device__ __forceinline__ void service_regs()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+}
+
+__device__ __forceinline__ void elementwise_regs()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+}
+
 // ---------------------------------------------------------------- packed fp32 pairs
 __device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi)
 {
@@ -36,6 +50,18 @@ __device__ __forceinline__ void unpair(uint64_t p, float &lo, float &hi)
     asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(p));
     lo = __uint_as_float(a);
     hi = __uint_as_float(b);
+}
+
+// Keeps the compiler from moving a pair's computation across this point.
+__device__ __forceinline__ void pair_fence(uint64_t &x)
+{
+    asm volatile("" : "+l"(x));
+}
+
+// Four consecutive fp32 of shared memory as two pairs; not moved across fences.
+__device__ __forceinline__ void lds_pairs(uint32_t addr, uint64_t &a, uint64_t &b)
+{
+    asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr));
 }
 
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
@@ -59,23 +85,56 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
     return r;
 }
 
-// 32 columns of an accumulator row, times f, to bf16 at dst.
-__device__ __forceinline__ void store_acc(uint32_t tacc, float f, __nv_bfloat16 *dst, bool row_ok)
+// 32 fp32 columns of an accumulator row (one row per lane), times f, as 16
+// packed bf16 pairs.
+__device__ __forceinline__ void load_acc(uint32_t tacc, float f, uint32_t (&o)[16])
 {
-    uint32_t o[32];
-    tmem_ld32_nowait(tacc, o);
+    uint32_t r[32];
+    tmem_ld32_nowait(tacc, r);
     tmem_wait_ld();
 #pragma unroll
     for (int i = 0; i < 32; ++i)
-        reg_fence(o[i]);
-    if (row_ok) {
+        reg_fence(r[i]);
 #pragma unroll
-        for (int i = 0; i < 32; i += 8)
-            *reinterpret_cast<uint4 *>(dst + i) =
-                make_uint4(pack_bf16x2(__uint_as_float(o[i]) * f, __uint_as_float(o[i + 1]) * f),
-                           pack_bf16x2(__uint_as_float(o[i + 2]) * f, __uint_as_float(o[i + 3]) * f),
-                           pack_bf16x2(__uint_as_float(o[i + 4]) * f, __uint_as_float(o[i + 5]) * f),
-                           pack_bf16x2(__uint_as_float(o[i + 6]) * f, __uint_as_float(o[i + 7]) * f));
+    for (int i = 0; i < 16; ++i)
+        o[i] = pack_bf16x2(__uint_as_float(r[2 * i]) * f, __uint_as_float(r[2 * i + 1]) * f);
+}
+
+// Stores such rows (64 bytes each, row i of the warp at dst + i * stride
+// elements, rows < n).  A lane's row is four 16-byte pieces; stored as they
+// are, every store would touch 32 lines.  The pieces are transposed within
+// quads of lanes first (two butterfly steps), so that a store covers 64 bytes
+// of eight rows.  Whole warp.
+__device__ __forceinline__ void store_rows(const uint32_t (&o)[16], __nv_bfloat16 *dst, long long stride, int n)
+{
+    const int lane = threadIdx.x & 31;
+    const bool odd = lane & 1, high = lane & 2;
+    uint4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        v[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+    auto swap = [](uint4 &a, uint4 &b, bool up, int m) {
+        // the lane keeps one of a, b and gets the other's counterpart from its partner
+        uint4 t = up ? a : b;
+        t.x = __shfl_xor_sync(kFull, t.x, m);
+        t.y = __shfl_xor_sync(kFull, t.y, m);
+        t.z = __shfl_xor_sync(kFull, t.z, m);
+        t.w = __shfl_xor_sync(kFull, t.w, m);
+        if (up)
+            a = t;
+        else
+            b = t;
+    };
+    swap(v[0], v[1], odd, 1);
+    swap(v[2], v[3], odd, 1);
+    swap(v[0], v[2], high, 2);
+    swap(v[1], v[3], high, 2);
+    // v[k]: piece lane & 3 of row (lane & ~3) + k
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int r = (lane & ~3) + k;
+        if (r < n)
+            *reinterpret_cast<uint4 *>(dst + r * stride + (lane & 3) * 8) = v[k];
     }
 }
 

@@ -97,6 +97,7 @@ struct Bars {
     uint64_t d_empty;               // kElemWarps arrivals: D has been read
     uint64_t p_full[2];             // kElemWarps arrivals: P and dS written
     uint64_t acc_full;              // the item's accumulators are complete
+    uint64_t acc_empty;             // kElemWarps arrivals: they have been read
     uint64_t mma_done[2];
     uint64_t desc_full[kDescRing];
     uint64_t desc_empty[kDescRing]; // kDescReaders arrivals
@@ -197,10 +198,10 @@ struct DescReader {
 // P = 0, and zeroed operands, so D = 0).  False if the wait for D ran out.
 template <bool kDQ>
 __device__ __forceinline__ bool elem_tile(uint32_t tS, uint32_t tD, int valid, float sl2, float neg_lse2,
-                                          float neg_delta, const float *col_lse2, const float *col_delta, Bars *bars,
+                                          float neg_delta, uint32_t cl, Bars *bars,
                                           uint32_t d_parity, const Params &p, volatile int *abort_flag)
 {
-    uint32_t s[kCols], d[kCols], pk[kCols / 2];
+    uint32_t s[kCols], pk[kCols / 2];
     tmem_ld32_nowait(tS, s);
     tmem_wait_ld();
 #pragma unroll
@@ -214,9 +215,7 @@ __device__ __forceinline__ bool elem_tile(uint32_t tS, uint32_t tD, int valid, f
         if (kDQ) {
             l0 = l1 = pair(neg_lse2, neg_lse2);
         } else {
-            const float4 l = reinterpret_cast<const float4 *>(col_lse2)[i];
-            l0 = pair(l.x, l.y);
-            l1 = pair(l.z, l.w);
+            lds_pairs(cl + 16 * i, l0, l1);
         }
         const uint64_t y0 = fma2(pair(s[4 * i], s[4 * i + 1]), k2, l0);
         const uint64_t y1 = fma2(pair(s[4 * i + 2], s[4 * i + 3]), k2, l1);
@@ -225,6 +224,10 @@ __device__ __forceinline__ bool elem_tile(uint32_t tS, uint32_t tD, int valid, f
         pr[2 * i] = pair(ex2_approx(a), ex2_approx(b));
         unpair(y1, a, b);
         pr[2 * i + 1] = pair(ex2_approx(a), ex2_approx(b));
+        if (!kDQ && (i & 1)) {   // at most two loads of column values ahead of their use
+            pair_fence(pr[2 * i]);
+            pair_fence(pr[2 * i + 1]);
+        }
     }
     if (!kDQ) {
 #pragma unroll
@@ -238,43 +241,47 @@ __device__ __forceinline__ bool elem_tile(uint32_t tS, uint32_t tD, int valid, f
     if (!wait_bar(smem_u32(&bars->d_full), d_parity, abort_flag, p.wait_ns, p.status))
         return false;
     tc_fence_after();
-    tmem_ld32_nowait(tD, d);
-    tmem_wait_ld();
+    // D in two halves: 16 registers fewer at once, which is what keeps the 96
+    // registers from spilling (beside 200 KB of shared memory spills live in L2)
 #pragma unroll
-    for (int i = 0; i < kCols; ++i)
-        reg_fence(d[i]);
-    tc_fence_before();
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0)
-        mbar_arrive(smem_u32(&bars->d_empty));
+    for (int h = 0; h < 2; ++h) {
+        uint32_t d[16], dk[8];
+        tmem_ld16_nowait(tD + 16 * h, d);
+        tmem_wait_ld();
 #pragma unroll
-    for (int i = 0; i < kCols / 4; ++i) {
-        uint64_t l0, l1;
-        if (kDQ) {
-            l0 = l1 = pair(neg_delta, neg_delta);
-        } else {
-            const float4 l = reinterpret_cast<const float4 *>(col_delta)[i];
-            l0 = pair(l.x, l.y);
-            l1 = pair(l.z, l.w);
+        for (int i = 0; i < 16; ++i)
+            reg_fence(d[i]);
+        if (h) {
+            tc_fence_before();
+            __syncwarp();
+            if ((threadIdx.x & 31) == 0)
+                mbar_arrive(smem_u32(&bars->d_empty));
         }
-        pr[2 * i] = mul2(pr[2 * i], add2(pair(d[4 * i], d[4 * i + 1]), l0));
-        pr[2 * i + 1] = mul2(pr[2 * i + 1], add2(pair(d[4 * i + 2], d[4 * i + 3]), l1));
-    }
-    if (kDQ && valid < kCols) {   // warp-uniform: the segment's last tile
 #pragma unroll
-        for (int i = 0; i < kCols / 2; ++i) {
+        for (int i = 0; i < 4; ++i) {
+            uint64_t l0, l1;
+            if (kDQ) {
+                l0 = l1 = pair(neg_delta, neg_delta);
+            } else {
+                lds_pairs(cl + 4 * kRows + 16 * (4 * h + i), l0, l1);
+            }
+            const uint64_t g0 = mul2(pr[8 * h + 2 * i], add2(pair(d[4 * i], d[4 * i + 1]), l0));
+            const uint64_t g1 = mul2(pr[8 * h + 2 * i + 1], add2(pair(d[4 * i + 2], d[4 * i + 3]), l1));
             float a, b;
-            unpair(pr[i], a, b);
-            pr[i] = pair(2 * i < valid ? a : 0.f, 2 * i + 1 < valid ? b : 0.f);
+            unpair(g0, a, b);
+            dk[2 * i] = pack_bf16x2(a, b);
+            unpair(g1, a, b);
+            dk[2 * i + 1] = pack_bf16x2(a, b);
         }
-    }
+        if (kDQ && valid < kCols) {   // warp-uniform: the segment's last tile
 #pragma unroll
-    for (int i = 0; i < kCols / 2; ++i) {
-        float a, b;
-        unpair(pr[i], a, b);
-        pk[i] = pack_bf16x2(a, b);
+            for (int i = 0; i < 8; ++i) {
+                const int c = 16 * h + 2 * i;
+                dk[i] = c + 1 < valid ? dk[i] : c < valid ? dk[i] & 0xffffu : 0u;
+            }
+        }
+        tmem_st8p(tS + kCols / 2 + 8 * h, dk);
     }
-    tmem_st16p(tS + kCols / 2, pk);
     tmem_wait_st();
     return true;
 }
@@ -310,6 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(smem_u32(&bars->d_full), 1);
         mbar_init(smem_u32(&bars->d_empty), kElemWarps);
         mbar_init(smem_u32(&bars->acc_full), 1);
+        mbar_init(smem_u32(&bars->acc_empty), kElemWarps);
         mbar_init(smem_u32(&bars->mma_done[0]), 1);
         mbar_init(smem_u32(&bars->mma_done[1]), 1);
         for (int j = 0; j < kDescRing; ++j) {
@@ -472,13 +480,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ======================================================== accumulating MMAs
         DescReader rd{0};
         ItemDesc d;
-        uint32_t nt = 0;
+        uint32_t nt = 0, n = 0;
         const uint64_t ring0 = smem_desc_sw128(ring_base, 0, 1024);
         const uint32_t id = idesc_bf16_f32(128, 64, true);
         bool ok = true;
         while (ok && rd.next(bars, p, abort_flag, d)) {
             const bool both = __shfl_sync(kFull, d.kind, 0) == 0;
             uint32_t acc = 0;
+            // the last item's accumulators have been read
+            if (n > 0 && !wait_bar(smem_u32(&bars->acc_empty), (n - 1) & 1, abort_flag, wait_ns, p.status))
+                break;
+            ++n;
             for (int left = __shfl_sync(kFull, d.T, 0); left > 0; left -= kRows, ++nt) {
                 const uint32_t s = nt % kRing, b = nt & 1;
                 if (!wait_bar(smem_u32(&bars->p_full[b]), (nt >> 1) & 1, abort_flag, wait_ns, p.status)) {
@@ -568,68 +580,109 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int g = (warp - kElem0) >> 2;   // warpgroup: columns 32g..32g+31
         const int qq = warp & 3;              // TMEM lane quarter of this warp
         const uint32_t lanes = (uint32_t)(qq * 32) << 16;
-        DescReader rd{0};
-        ItemDesc d;
-        int nt = 0, n = 0;
-        bool ok = true;
-        for (; ok && rd.next(bars, p, abort_flag, d); ++n) {
-            const int row = qq * 32 + lane;
-            const bool active = qq * 32 < d.rows;   // warp-uniform
-            const bool row_ok = row < d.rows;
-            float neg_lse2 = 0.f, neg_delta = 0.f;
-            if (d.kind == 1 && row_ok) {
-                const size_t at = (size_t)d.h * p.total + d.f0 + row;
-                neg_lse2 = __ldg(p.lse + at) * -kLog2e;
-                neg_delta = -__ldg(p.delta + at);
-            }
-            for (int left = d.T; left > 0; left -= kRows, ++nt) {
-                const int b = nt & 1, s = nt % (int)kRing;
-                const int valid = min(kRows, left) - kCols * g;   // columns of this warpgroup inside the segment
-                // kind 0: the tile's lse and delta were staged before t_ready
-                if ((d.kind == 0 && !wait_bar(smem_u32(&bars->t_ready[s]), (uint32_t)(nt / (int)kRing) & 1, abort_flag,
-                                              wait_ns, p.status)) ||
-                    !wait_bar(smem_u32(&bars->s_full[b]), ((uint32_t)nt >> 1) & 1, abort_flag, wait_ns, p.status)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                if (active && valid > 0) {
-                    const uint32_t tS = tmem + b * 128 + kCols * g + lanes, tD = tmem + kDCol + kCols * g + lanes;
-                    const float *cl = cols + s * (2 * kRows) + kCols * g;
-                    ok = d.kind ? elem_tile<true>(tS, tD, valid, p.scale_log2, neg_lse2, neg_delta, cl, cl + kRows,
-                                                  bars, (uint32_t)nt & 1, p, abort_flag)
-                                : elem_tile<false>(tS, tD, valid, p.scale_log2, neg_lse2, neg_delta, cl, cl + kRows,
-                                                   bars, (uint32_t)nt & 1, p, abort_flag);
-                } else {
-                    ok = wait_bar(smem_u32(&bars->d_full), (uint32_t)nt & 1, abort_flag, wait_ns, p.status);
+        const int row = qq * 32 + lane;
+        // Items are read from the ring where they are needed (registers are
+        // scarce); an entry is released once its results are stored.
+        auto item = [&](uint32_t k) -> const volatile ItemDesc & { return bars->desc[k % kDescRing]; };
+        auto arrived = [&](uint32_t k) -> bool {   // item k is published and is not the end marker
+            return wait_bar(smem_u32(&bars->desc_full[k % kDescRing]), (k / kDescRing) & 1, abort_flag, wait_ns,
+                            p.status) &&
+                   item(k).rows >= 0;
+        };
+        // kind 1: lse and delta of this lane's row
+        auto fetch = [&](uint32_t k, float &l, float &dl) {
+            const bool in = item(k).kind == 1 && row < item(k).rows;
+            const size_t at = (size_t)item(k).h * p.total + item(k).f0 + row;
+            l = in ? __ldg(p.lse + at) : 0.f;
+            dl = in ? __ldg(p.delta + at) : 0.f;
+        };
+        uint32_t nt = 0, n = 0;   // tiles; the current item
+        float vl = 0.f, vd = 0.f;
+        bool have = arrived(0), ok = true, pending = false;
+        if (have)
+            fetch(0, vl, vd);
+        // One pass per item, and a last one that only stores.  An item's
+        // results are stored after the next one's first tile, so that its
+        // last MMAs run under that tile's arithmetic; the next item's row
+        // values travel while the item's last tile is computed.
+        for (;;) {
+            const bool active = have && qq * 32 < item(n).rows;   // warp-uniform
+            const bool kq = have && item(n).kind == 1;
+            const float neg_lse2 = vl * -kLog2e, neg_delta = -vd;
+            bool more = false;
+            for (int left = have ? item(n).T : 0;; left -= kRows) {
+                if (left > 0) {
+                    const uint32_t b = nt & 1, s = nt % kRing;
+                    const int valid = min(kRows, left) - kCols * g;   // columns of this warpgroup inside the segment
+                    // kind 0: the tile's lse and delta were staged before t_ready
+                    if ((!kq && !wait_bar(smem_u32(&bars->t_ready[s]), (nt / kRing) & 1, abort_flag, wait_ns,
+                                          p.status)) ||
+                        !wait_bar(smem_u32(&bars->s_full[b]), (nt >> 1) & 1, abort_flag, wait_ns, p.status)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    if (left <= kRows) {
+                        more = arrived(n + 1);
+                        if (more)
+                            fetch(n + 1, vl, vd);
+                    }
+                    if (active && valid > 0) {
+                        const uint32_t tS = tmem + b * 128 + kCols * g + lanes, tD = tmem + kDCol + kCols * g + lanes;
+                        const uint32_t cl = smem_u32(cols) + 4 * (s * (2 * kRows) + kCols * g);
+                        ok = kq ? elem_tile<true>(tS, tD, valid, p.scale_log2, neg_lse2, neg_delta, cl, bars, nt & 1, p,
+                                                  abort_flag)
+                                : elem_tile<false>(tS, tD, valid, p.scale_log2, neg_lse2, neg_delta, cl, bars, nt & 1,
+                                                   p, abort_flag);
+                    } else {
+                        ok = wait_bar(smem_u32(&bars->d_full), nt & 1, abort_flag, wait_ns, p.status);
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(smem_u32(&bars->d_empty));
+                    }
+                    if (!ok)
+                        break;
+                    tc_fence_before();
                     __syncwarp();
                     if (lane == 0)
-                        mbar_arrive(smem_u32(&bars->d_empty));
+                        mbar_arrive(smem_u32(&bars->p_full[b]));
+                    ++nt;
                 }
-                if (!ok)
+                if (pending) {
+                    // ---------------------------------------------- output rows
+                    if (!wait_bar(smem_u32(&bars->acc_full), (n - 1) & 1, abort_flag, wait_ns, p.status)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    // kind 0: warpgroups 0, 1 store dK, 2, 3 dV; kind 1: 0, 1 store dQ
+                    const bool pq = item(n - 1).kind == 1;
+                    const int rows = item(n - 1).rows - qq * 32;
+                    const bool mine = rows > 0 && (!pq || g < 2);
+                    const int c = 32 * (g & 1);
+                    uint32_t o[16];
+                    if (mine)
+                        load_acc(tmem + (g < 2 ? kAcc0 : kAcc1) + c + lanes, g < 2 ? p.scale : 1.f, o);
+                    __nv_bfloat16 *dst = (pq ? p.dq : g < 2 ? p.dk : p.dv) +
+                                         (item(n - 1).f0 + qq * 32) * p.out_stride + item(n - 1).h * 64 + c;
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(smem_u32(&bars->acc_empty));
+                        mbar_arrive(smem_u32(&bars->desc_empty[(n - 1) % kDescRing]));
+                    }
+                    if (mine)
+                        store_rows(o, dst, p.out_stride, rows);
+                    pending = false;
+                }
+                if (left <= kRows)
                     break;
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(smem_u32(&bars->p_full[b]));
             }
-            if (!ok)
+            if (!ok || !have)
                 break;
-            // ---------------------------------------------- output rows
-            if (!wait_bar(smem_u32(&bars->acc_full), (uint32_t)n & 1, abort_flag, wait_ns, p.status))
-                break;
-            tc_fence_after();
-            if (active) {
-                const long long at = (long long)(d.f0 + row) * p.out_stride + d.h * 64;
-                // kind 0: warpgroups 0, 1 store dK, 2, 3 dV; kind 1: 0, 1 store dQ
-                const int c = 32 * (g & 1);
-                if (d.kind == 0)
-                    store_acc(tmem + (g < 2 ? kAcc0 : kAcc1) + c + lanes, g < 2 ? p.scale : 1.f,
-                              (g < 2 ? p.dk : p.dv) + at + c, row_ok);
-                else if (g < 2)
-                    store_acc(tmem + kAcc0 + c + lanes, p.scale, p.dq + at + c, row_ok);
-            }
-            tc_fence_before();
+            pending = true;
+            ++n;
+            have = more;
         }
     }
 

@@ -16,7 +16,8 @@
 // dS is written once, as 64-query chunks of 128-byte rows (one key each),
 // 128-byte swizzled: a row-major operand for dK and a column-major one for dQ.
 //
-// One persistent CTA per SM, 20 warps:
+// One persistent CTA per SM, 12 warps (168 registers; 20 warps of 96 spilled,
+// and beside 210 KB of shared memory the spills live in L2: twice the time):
 //   warp 0   TMA producer: K, Q, V, dO of an item, one box each, into a ring
 //            of matrix slots; publishes the item's descriptor.
 //   warp 1   issues S and D.
@@ -24,14 +25,12 @@
 //   warp 3   owns TMEM; zeroes operand rows past the block (up to the MMAs'
 //            16-row granule: their P and dS are 0, but 0 * Inf would be NaN)
 //            and stages the block's lse and delta (+inf and 0 past it).
-//   warps 4-19  elementwise, two groups of eight warps on alternate units
-//            (group g: S, D buffer g): a lane owns one key of the tile, a
-//            warp half of the unit's columns.  They also store the results:
-//            a key tile's after the first unit of the next, so that its last
-//            MMAs run under arithmetic.
-// TMEM (512 columns): S, D of group g at 128 g and 128 g + 64 (P over S: warp
-// half j's in columns 32j..32j+15), dQ_0, dQ_1 at 256 and 320, dK at 384, dV
-// at 448.
+//   warps 4-11  elementwise, two groups of four warps on alternate units
+//            (group g: S, D buffer g): a lane owns one key of the tile.  They
+//            also store the results: a key tile's after the first unit of the
+//            next, so that its last MMAs run under arithmetic.
+// TMEM (512 columns): S, D of group g at 128 g and 128 g + 64 (P over S's
+// first 32 columns), dQ_0, dQ_1 at 256 and 320, dK at 384, dV at 448.
 //
 // Every mbarrier wait is bounded; on expiry the CTA drains its copies and
 // MMAs in flight, frees TMEM and returns.
@@ -47,11 +46,10 @@ namespace {
 using namespace nle;
 
 constexpr int kElem0 = 4;                            // first elementwise warp
-constexpr int kElemWarps = 16;                       // two groups of eight
-constexpr int kThreads = 32 * (kElem0 + kElemWarps); // 640
+constexpr int kElemWarps = 8;                        // two groups of four
+constexpr int kThreads = 32 * (kElem0 + kElemWarps); // 384
 constexpr int kKeys = 128;                           // keys of a tile (MMA M)
 constexpr int kUnit = 64;                            // queries of a unit
-constexpr int kCols = 32;                            // columns of an elementwise warp
 constexpr int kRowBytes = 128;                       // one frame of one head: 64 bf16
 constexpr uint32_t kTileBytes = kKeys * kRowBytes;   // 16 KB
 constexpr uint32_t kChunkBytes = kKeys * kRowBytes;  // dS of a unit: 128 keys x 64 queries
@@ -72,8 +70,8 @@ struct Bars {
     uint64_t ready[2];              // by item: matrices checked, columns staged
     uint64_t cols_empty[2];         // kElemWarps arrivals: the item's columns are no longer read
     uint64_t s_full[2], d_full[2];  // by group
-    uint64_t d_empty[2];            // 8 arrivals: D has been read
-    uint64_t p_full[2];             // 8 arrivals: P and dS written
+    uint64_t d_empty[2];            // 4 arrivals: D has been read
+    uint64_t p_full[2];             // 4 arrivals: P and dS written
     uint64_t p_empty[2];            // the unit's dV and dK MMAs have completed (P)
     uint64_t dq_done[2];            // the key tile's dQ_x MMAs have completed (dS chunks 2x, 2x + 1)
     uint64_t acc_full;              // the key tile's sums (the item's, on its last) are complete
@@ -115,6 +113,107 @@ struct DescReader {
         return d.L >= 0;
     }
 };
+
+// A unit for a warp without keys in the tile: it only keeps the barriers' count.
+__device__ __forceinline__ bool unit_idle(Bars *bars, int g, int x, uint32_t use, uint32_t nx, const Params &p,
+                                          volatile int *abort_flag)
+{
+    if (!wait_bar(smem_u32(&bars->s_full[g]), use & 1, abort_flag, p.wait_ns, p.status) ||
+        !wait_bar(smem_u32(&bars->d_full[g]), use & 1, abort_flag, p.wait_ns, p.status))
+        return false;
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0)
+        mbar_arrive(smem_u32(&bars->d_empty[g]));
+    return nx == 0 || wait_bar(smem_u32(&bars->dq_done[x]), (nx - 1) & 1, abort_flag, p.wait_ns, p.status);
+}
+
+// A unit for one lane (one key): P of its 32 * NH queries to TMEM over S, dS
+// to the lane's row of the shared-memory chunk (128-byte swizzle).  cl: the
+// queries' -lse log2e, and 256 floats on their -delta.  Keys past the block
+// (not row_ok) give dS = 0: dQ sums over all keys of the MMAs' 16-row granule.
+template <int NH>
+__device__ __forceinline__ bool unit_work(uint32_t tS, const float *cl, uint8_t *dst, int row, bool row_ok, Bars *bars,
+                                          int g, int x, uint32_t use, uint32_t nx, const Params &p,
+                                          volatile int *abort_flag)
+{
+    if (!wait_bar(smem_u32(&bars->s_full[g]), use & 1, abort_flag, p.wait_ns, p.status))
+        return false;
+    tc_fence_after();
+    uint32_t s[32 * NH];
+#pragma unroll
+    for (int h = 0; h < NH; ++h)
+        tmem_ld32_nowait(tS + 32 * h, s + 32 * h);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 32 * NH; ++i)
+        reg_fence(s[i]);
+    const uint64_t k2 = pair(p.scale_log2, p.scale_log2);
+    uint64_t pr[16 * NH];
+#pragma unroll
+    for (int h = 0; h < NH; ++h) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int q = 8 * h + i;
+            const float4 l = reinterpret_cast<const float4 *>(cl)[q];
+            const uint64_t y0 = fma2(pair(s[4 * q], s[4 * q + 1]), k2, pair(l.x, l.y));
+            const uint64_t y1 = fma2(pair(s[4 * q + 2], s[4 * q + 3]), k2, pair(l.z, l.w));
+            float a, b;
+            unpair(y0, a, b);
+            a = ex2_approx(a);
+            b = ex2_approx(b);
+            pr[2 * q] = pair(a, b);
+            pk[2 * i] = pack_bf16x2(a, b);
+            unpair(y1, a, b);
+            a = ex2_approx(a);
+            b = ex2_approx(b);
+            pr[2 * q + 1] = pair(a, b);
+            pk[2 * i + 1] = pack_bf16x2(a, b);
+        }
+        tmem_st16p(tS + 16 * h, pk);
+    }
+    if (!wait_bar(smem_u32(&bars->d_full[g]), use & 1, abort_flag, p.wait_ns, p.status))
+        return false;
+    // the last key tile's dQ no longer reads this half's chunks
+    if (nx > 0 && !wait_bar(smem_u32(&bars->dq_done[x]), (nx - 1) & 1, abort_flag, p.wait_ns, p.status))
+        return false;
+    tc_fence_after();
+#pragma unroll
+    for (int h = 0; h < NH; ++h) {
+        uint32_t d[32];
+        tmem_ld32_nowait(tS + kDCol + 32 * h, d);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            reg_fence(d[i]);
+        if (h == NH - 1) {   // D has been read
+            tc_fence_before();
+            __syncwarp();
+            if ((threadIdx.x & 31) == 0)
+                mbar_arrive(smem_u32(&bars->d_empty[g]));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t pk[4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int q = 2 * i + j, r = 8 * h + q;
+                const float4 l = reinterpret_cast<const float4 *>(cl + 256)[r];
+                const uint64_t g0 = mul2(pr[2 * r], add2(pair(d[4 * q], d[4 * q + 1]), pair(l.x, l.y)));
+                const uint64_t g1 = mul2(pr[2 * r + 1], add2(pair(d[4 * q + 2], d[4 * q + 3]), pair(l.z, l.w)));
+                float a, b;
+                unpair(g0, a, b);
+                pk[2 * j] = row_ok ? pack_bf16x2(a, b) : 0u;
+                unpair(g1, a, b);
+                pk[2 * j + 1] = row_ok ? pack_bf16x2(a, b) : 0u;
+            }
+            *reinterpret_cast<uint4 *>(dst + ((4 * h + i) ^ (row & 7)) * 16) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+        }
+    }
+    fence_proxy_async_smem();
+    tmem_wait_st();
+    return true;
+}
 
 // Results waiting to be stored: a key tile's dK, dV and, with its item's
 // last tile, the item's dQ.
@@ -348,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (kk < steps) {
                                 const uint64_t row = ub + kk * (16 * kRowBytes >> 4);
                                 const uint32_t acc = u > 0 || kk > 0 ? 1u : 0u;
-                                mma_ts(tmem + kVAcc, ap + (kk >> 1) * 32 + (kk & 1) * 8, bo + row, id, acc);
+                                mma_ts(tmem + kVAcc, ap + kk * 8, bo + row, id, acc);
                                 mma_ss(tmem + kKAcc, ak + 2 * kk, bq + row, id, acc);
                             }
                         }
@@ -427,167 +526,100 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         // ======================================================== elementwise
         const int e = warp - kElem0;
-        const int g = e >> 3, half = (e >> 2) & 1;   // group; half of the unit's columns
+        const int g = e >> 2;                        // group
         const int qq = warp & 3;                     // TMEM lane quarter of this warp
         const int row = qq * 32 + lane;              // key of the tile
         const uint32_t lanes = (uint32_t)(qq * 32) << 16;
-        const uint32_t tS = tmem + g * kGroupCols + kCols * half + lanes;
-        const uint64_t k2 = pair(p.scale_log2, p.scale_log2);
+        const uint32_t tS = tmem + g * kGroupCols + lanes;
         DescReader rd{0};
-        ItemDesc d;
-        uint32_t n = 0, t = 0, kt = 0;       // items, units, key tiles
-        uint32_t nx[2] = {0, 0};             // key tiles that had queries in half x of the block
-        Pending pend{};
-        bool ok = true;
-
-        // Stores the pending results once they are complete.
-        auto store = [&]() -> bool {
-            if (!pend.have)
-                return true;
-            pend.have = false;
-            if (!wait(&bars->acc_full, kt - 1))
-                return false;
-            tc_fence_after();
-            // dK by the first group, dV by the second; half of the columns per warp
-            const int nk = pend.L - pend.c * kKeys;
-            const int f = pend.f0 + pend.c * kKeys + row;
-            if (qq * 32 < nk)
-                store_acc(tmem + (g ? kVAcc : kKAcc) + kCols * half + lanes, g ? 1.f : p.scale,
-                          (g ? p.dv : p.dk) + (long long)f * p.out_stride + pend.h * 64 + kCols * half, row < nk);
-            if (pend.last) {   // dQ of queries 128 g .. by group g
-                const int nq = pend.L - g * kKeys;
-                if (qq * 32 < nq)
-                    store_acc(tmem + kQAcc + 64 * g + kCols * half + lanes, p.scale,
-                              p.dq + (long long)(pend.f0 + g * kKeys + row) * p.out_stride + pend.h * 64 + kCols * half,
-                              row < nq);
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(smem_u32(&bars->acc_empty));
-            return true;
-        };
-
-        for (; ok && rd.next(bars, p, abort_flag, d); ++n) {
-            if (!wait(&bars->ready[n & 1], n >> 1)) {
-                ok = false;
-                break;
-            }
-            const float *cl = cols + (n & 1) * 512;
-            for (int c = 0; ok && c * kKeys < d.L; ++c) {
-                const bool active = c * kKeys + qq * 32 < d.L;   // warp-uniform
-                const bool row_ok = c * kKeys + row < d.L;
-                for (int u = 0; u * kUnit < d.L; ++u, ++t) {
-                    if ((t & 1) != (uint32_t)g)
-                        continue;
-                    const uint32_t use = t >> 1;
-                    const int c0 = u * kUnit + kCols * half;   // first query of the warp's columns
-                    const int x = u >> 1;
-                    if (!wait(&bars->s_full[g], use)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const bool work = active && c0 < d.L;      // warp-uniform
-                    uint64_t pr[kCols / 2];
-                    uint32_t pk[kCols / 2];
-                    if (work) {
-                        uint32_t s[kCols];
-                        tmem_ld32_nowait(tS, s);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < kCols; ++i)
-                            reg_fence(s[i]);
-#pragma unroll
-                        for (int i = 0; i < kCols / 4; ++i) {
-                            const float4 l = reinterpret_cast<const float4 *>(cl + c0)[i];
-                            const uint64_t y0 = fma2(pair(s[4 * i], s[4 * i + 1]), k2, pair(l.x, l.y));
-                            const uint64_t y1 = fma2(pair(s[4 * i + 2], s[4 * i + 3]), k2, pair(l.z, l.w));
-                            float a, b;
-                            unpair(y0, a, b);
-                            pr[2 * i] = pair(ex2_approx(a), ex2_approx(b));
-                            unpair(y1, a, b);
-                            pr[2 * i + 1] = pair(ex2_approx(a), ex2_approx(b));
-                        }
-#pragma unroll
-                        for (int i = 0; i < kCols / 2; ++i) {
-                            float a, b;
-                            unpair(pr[i], a, b);
-                            pk[i] = pack_bf16x2(a, b);
-                        }
-                        tmem_st16p(tS, pk);
-                    }
-                    if (!wait(&bars->d_full[g], use)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    if (work) {
-                        uint32_t dd[kCols];
-                        tmem_ld32_nowait(tS + kDCol, dd);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < kCols; ++i)
-                            reg_fence(dd[i]);
-#pragma unroll
-                        for (int i = 0; i < kCols / 4; ++i) {
-                            const float4 l = reinterpret_cast<const float4 *>(cl + 256 + c0)[i];
-                            pr[2 * i] = mul2(pr[2 * i], add2(pair(dd[4 * i], dd[4 * i + 1]), pair(l.x, l.y)));
-                            pr[2 * i + 1] = mul2(pr[2 * i + 1], add2(pair(dd[4 * i + 2], dd[4 * i + 3]), pair(l.z, l.w)));
-                        }
-#pragma unroll
-                        for (int i = 0; i < kCols / 2; ++i) {
-                            float a, b;
-                            unpair(pr[i], a, b);
-                            // keys past the block: nothing to dQ
-                            pk[i] = row_ok ? pack_bf16x2(a, b) : 0u;
-                        }
-                    }
-                    tc_fence_before();
+        ItemDesc d{0, 0, 0};
+        uint32_t n = 0, t = 0, kt = 0;       // items and key tiles begun; units before the tile
+        uint32_t nx0 = 0, nx1 = 0;           // key tiles that had queries in half 0, 1 of the block
+        int c = 0;                           // the item's current key tile
+        Pending pend{0, 0, 0, 0, false, false};
+        // One pass per key tile, and a last one that only stores.
+        for (;;) {
+            if (c * kKeys >= d.L) {   // the next item
+                if (n > 0) {
                     __syncwarp();
                     if (lane == 0)
-                        mbar_arrive(smem_u32(&bars->d_empty[g]));
-                    // the last key tile's dQ no longer reads these chunks
-                    if (nx[x] > 0 && !wait(&bars->dq_done[x], nx[x] - 1)) {
-                        ok = false;
+                        mbar_arrive(smem_u32(&bars->cols_empty[(n - 1) & 1]));
+                }
+                c = 0;
+                if (!rd.next(bars, p, abort_flag, d))
+                    d.L = 0;   // no further item (or a wait ran out: the next one returns at once)
+                else if (!wait(&bars->ready[n & 1], n >> 1))
+                    break;
+                ++n;
+            }
+            const float *cl = cols + ((n - 1) & 1) * 512;
+            const bool active = c * kKeys + qq * 32 < d.L;   // warp-uniform
+            const bool row_ok = c * kKeys + row < d.L;
+            bool ok = true;
+            // the group's units of the tile
+            for (int u = (t ^ g) & 1;; u += 2) {
+                const bool have = u * kUnit < d.L;
+                if (have) {
+                    const uint32_t use = (t + u) >> 1;
+                    const int c0 = u * kUnit;           // first query of the unit
+                    const bool two = c0 + 32 < d.L;    // warp-uniform: queries in the unit's second half
+                    const uint32_t nx = u >> 1 ? nx1 : nx0;
+                    uint8_t *dst = smem + p.ds_off + u * kChunkBytes + row * kRowBytes;
+                    ok = !active ? unit_idle(bars, g, u >> 1, use, nx, p, abort_flag)
+                         : two   ? unit_work<2>(tS, cl + c0, dst, row, row_ok, bars, g, u >> 1, use, nx, p, abort_flag)
+                                 : unit_work<1>(tS, cl + c0, dst, row, row_ok, bars, g, u >> 1, use, nx, p, abort_flag);
+                    if (!ok)
                         break;
-                    }
-                    if (work) {
-                        uint8_t *dst = smem + p.ds_off + u * kChunkBytes + row * kRowBytes;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            *reinterpret_cast<uint4 *>(dst + ((4 * half + i) ^ (row & 7)) * 16) =
-                                make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
-                        fence_proxy_async_smem();
-                        tmem_wait_st();
-                    }
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0)
                         mbar_arrive(smem_u32(&bars->p_full[g]));
-                    if (!store()) {
+                }
+                if (pend.have) {
+                    // the last key tile's results: dK by the first group, dV
+                    // by the second, and with an item's last tile dQ of
+                    // queries 128 g .. by group g
+                    pend.have = false;
+                    if (!wait(&bars->acc_full, kt - 1)) {
                         ok = false;
                         break;
                     }
+                    tc_fence_after();
+                    const int nk = pend.L - pend.c * kKeys - qq * 32, nq = pend.last ? pend.L - g * kKeys - qq * 32 : 0;
+                    uint32_t a[2][16], b[2][16];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (nk > 0)
+                            load_acc(tmem + (g ? kVAcc : kKAcc) + 32 * h + lanes, g ? 1.f : p.scale, a[h]);
+                        if (nq > 0)
+                            load_acc(tmem + kQAcc + 64 * g + 32 * h + lanes, p.scale, b[h]);
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(smem_u32(&bars->acc_empty));
+                    __nv_bfloat16 *da = (g ? p.dv : p.dk) + (pend.f0 + pend.c * kKeys + qq * 32) * p.out_stride + pend.h * 64;
+                    __nv_bfloat16 *db = p.dq + (pend.f0 + g * kKeys + qq * 32) * p.out_stride + pend.h * 64;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (nk > 0)
+                            store_rows(a[h], da + 32 * h, p.out_stride, nk);
+                        if (nq > 0)
+                            store_rows(b[h], db + 32 * h, p.out_stride, nq);
+                    }
                 }
-                if (!ok || !store()) {   // a tile without a unit for this group
-                    ok = false;
+                if (!have)
                     break;
-                }
-                ++nx[0];
-                if (d.L > kKeys)
-                    ++nx[1];
-                pend = Pending{d.f0, d.L, d.h, c, true, (c + 1) * kKeys >= d.L};
-                ++kt;
             }
-            if (!ok)
+            if (!ok || d.L == 0)
                 break;
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(smem_u32(&bars->cols_empty[n & 1]));
+            t += (d.L + kUnit - 1) / kUnit;
+            ++nx0;
+            nx1 += d.L > kKeys;
+            pend = Pending{d.f0, d.L, d.h, c, true, (c + 1) * kKeys >= d.L};
+            ++kt;
+            ++c;
         }
-        if (ok)
-            store();
     }
 
     // ------------------------------------------------------------ teardown
