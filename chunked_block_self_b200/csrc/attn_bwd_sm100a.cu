@@ -60,23 +60,26 @@ namespace {
 using namespace nle;
 
 constexpr int kElem0 = 4;                            // first elementwise warp
-constexpr int kElemWarps = 16;                       // four warpgroups
+constexpr int kElemWarps = 16;                       // four groups of four, one per TMEM lane quarter
 constexpr int kThreads = 32 * (kElem0 + kElemWarps); // 640
-constexpr int kCols = 32;                            // tile columns of a warpgroup
-constexpr int kRows = 128;                           // owner rows, and rows of a tile
+constexpr int kCols = 32;                            // tile columns of a group
+constexpr int kRows = 128;                           // owner rows
+constexpr int kTile = 64;                            // rows of a tile
 constexpr int kRowBytes = 128;                       // one frame of one head: 64 bf16
-constexpr uint32_t kMatBytes = kRows * kRowBytes;    // 16 KB
-constexpr uint32_t kPairBytes = 2 * kMatBytes;       // X, Y (owner) or x, y (tile)
-constexpr uint32_t kColBytes = 2 * kRows * 4;        // a tile's -lse (log2 domain) and -delta
-constexpr uint32_t kRing = 4;                        // tiles in flight
+constexpr uint32_t kBoxBytes = kTile * kRowBytes;    // 8 KB: every TMA box is 64 frames
+constexpr uint32_t kMatBytes = kRows * kRowBytes;    // X or Y: 16 KB
+constexpr uint32_t kPairBytes = 2 * kMatBytes;       // X, Y
+constexpr uint32_t kStageBytes = 2 * kBoxBytes;      // x, y
+constexpr uint32_t kColBytes = 2 * kCols * 4;        // an elementwise warp's columns: -lse (log2 domain), -delta
+constexpr uint32_t kRing = 8;                        // tiles in flight
 constexpr int kDescRing = 4;
-constexpr int kDescReaders = 3 + kElemWarps;         // both MMA, fix-up and elementwise warps
+constexpr int kDescReaders = 3 + kElemWarps;         // S, D, accumulating and elementwise warps
 // shared memory: two owner stages, the tile ring, the tiles' columns, the barriers
 constexpr uint32_t kRingOff = 2 * kPairBytes;
-constexpr uint32_t kColOff = kRingOff + kRing * kPairBytes;
-constexpr uint32_t kBarsOff = kColOff + kRing * kColBytes;
+constexpr uint32_t kColOff = kRingOff + kRing * kStageBytes;
+constexpr uint32_t kBarsOff = kColOff + kElemWarps * kColBytes;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kDCol = 256, kAcc0 = 384, kAcc1 = 448;
+constexpr uint32_t kStreamCols = 192, kDCol = 128, kAcc0 = 384, kAcc1 = 448;
 
 // One work item as the producer publishes it (rows < 0: no further item).
 struct ItemDesc {
@@ -87,18 +90,17 @@ struct ItemDesc {
 
 struct Bars {
     uint64_t own_full[2];
-    uint64_t own_empty[2];          // the item's last S and D MMAs have completed
+    uint64_t own_empty[2];          // 2 arrivals: the item's last S and last D MMA have completed
     uint64_t t_full[kRing];
-    uint64_t t_ready[kRing];     // the fix-up warp has checked the tile
     uint64_t t_empty[kRing];     // the tile's accumulating MMAs have completed
-    uint64_t s_full[2];
-    uint64_t s_empty[2];            // the accumulating MMAs that read P, dS have completed
-    uint64_t d_full;
-    uint64_t d_empty;               // kElemWarps arrivals: D has been read
-    uint64_t p_full[2];             // kElemWarps arrivals: P and dS written
+    uint64_t s_full[4];             // by tile & 3
+    uint64_t s_empty[4];            // the accumulating MMAs that read P, dS have completed
+    uint64_t p_full[4];             // kElemWarps / 2 arrivals: P and dS written
+    uint64_t d_full[2];             // by tile & 1
+    uint64_t d_empty[2];            // kElemWarps / 2 arrivals: D has been read
     uint64_t acc_full;              // the item's accumulators are complete
     uint64_t acc_empty;             // kElemWarps arrivals: they have been read
-    uint64_t mma_done[2];
+    uint64_t mma_done[3];
     uint64_t desc_full[kDescRing];
     uint64_t desc_empty[kDescRing]; // kDescReaders arrivals
     ItemDesc desc[kDescRing];
@@ -199,7 +201,7 @@ struct DescReader {
 template <bool kDQ>
 __device__ __forceinline__ bool elem_tile(uint32_t tS, uint32_t tD, int valid, float sl2, float neg_lse2,
                                           float neg_delta, uint32_t cl, Bars *bars,
-                                          uint32_t d_parity, const Params &p, volatile int *abort_flag)
+                                          int stream, uint32_t d_parity, const Params &p, volatile int *abort_flag)
 {
     uint32_t s[kCols], pk[kCols / 2];
     tmem_ld32_nowait(tS, s);
@@ -238,7 +240,7 @@ __device__ __forceinline__ bool elem_tile(uint32_t tS, uint32_t tD, int valid, f
         }
         tmem_st16p(tS, pk);
     }
-    if (!wait_bar(smem_u32(&bars->d_full), d_parity, abort_flag, p.wait_ns, p.status))
+    if (!wait_bar(smem_u32(&bars->d_full[stream]), d_parity, abort_flag, p.wait_ns, p.status))
         return false;
     tc_fence_after();
     // D in two halves: 16 registers fewer at once, which is what keeps the 96
@@ -255,7 +257,7 @@ __device__ __forceinline__ bool elem_tile(uint32_t tS, uint32_t tD, int valid, f
             tc_fence_before();
             __syncwarp();
             if ((threadIdx.x & 31) == 0)
-                mbar_arrive(smem_u32(&bars->d_empty));
+                mbar_arrive(smem_u32(&bars->d_empty[stream]));
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -263,7 +265,7 @@ __device__ __forceinline__ bool elem_tile(uint32_t tS, uint32_t tD, int valid, f
             if (kDQ) {
                 l0 = l1 = pair(neg_delta, neg_delta);
             } else {
-                lds_pairs(cl + 4 * kRows + 16 * (4 * h + i), l0, l1);
+                lds_pairs(cl + 4 * kCols + 16 * (4 * h + i), l0, l1);
             }
             const uint64_t g0 = mul2(pr[8 * h + 2 * i], add2(pair(d[4 * i], d[4 * i + 1]), l0));
             const uint64_t g1 = mul2(pr[8 * h + 2 * i + 1], add2(pair(d[4 * i + 2], d[4 * i + 3]), l1));
@@ -295,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t own_base = smem_u32(smem);
     const uint32_t ring_base = own_base + kRingOff;
-    float *cols = reinterpret_cast<float *>(smem + kColOff);   // per stage: -lse2[128], -delta[128]
+    float *cols = reinterpret_cast<float *>(smem + kColOff);   // per elementwise warp: -lse2[32], -delta[32]
     Bars *bars = reinterpret_cast<Bars *>(smem + kBarsOff);
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -304,22 +306,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_u32(&bars->own_full[s]), 1);
-            mbar_init(smem_u32(&bars->own_empty[s]), 1);
+            mbar_init(smem_u32(&bars->own_empty[s]), 2);
+            mbar_init(smem_u32(&bars->d_full[s]), 1);
+            mbar_init(smem_u32(&bars->d_empty[s]), kElemWarps / 2);
+        }
+        for (int s = 0; s < 4; ++s) {
             mbar_init(smem_u32(&bars->s_full[s]), 1);
             mbar_init(smem_u32(&bars->s_empty[s]), 1);
-            mbar_init(smem_u32(&bars->p_full[s]), kElemWarps);
+            mbar_init(smem_u32(&bars->p_full[s]), kElemWarps / 2);
         }
         for (int s = 0; s < (int)kRing; ++s) {
             mbar_init(smem_u32(&bars->t_full[s]), 1);
-            mbar_init(smem_u32(&bars->t_ready[s]), 1);
             mbar_init(smem_u32(&bars->t_empty[s]), 1);
         }
-        mbar_init(smem_u32(&bars->d_full), 1);
-        mbar_init(smem_u32(&bars->d_empty), kElemWarps);
         mbar_init(smem_u32(&bars->acc_full), 1);
         mbar_init(smem_u32(&bars->acc_empty), kElemWarps);
-        mbar_init(smem_u32(&bars->mma_done[0]), 1);
-        mbar_init(smem_u32(&bars->mma_done[1]), 1);
+        for (int s = 0; s < 3; ++s)
+            mbar_init(smem_u32(&bars->mma_done[s]), 1);
         for (int j = 0; j < kDescRing; ++j) {
             mbar_init(smem_u32(&bars->desc_full[j]), 1);
             mbar_init(smem_u32(&bars->desc_empty[j]), kDescReaders);
@@ -381,13 +384,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0 && !(skip0 && nown == 0)) {
                 const uint32_t bar = smem_u32(&bars->own_full[os]);
                 const uint32_t dst = own_base + os * kPairBytes;
-                mbar_arrive_expect_tx(bar, kPairBytes);
-                tma_load(dst, d.kind ? &tm_q : &tm_k, d.h * 64, d.f0, bar);
-                tma_load(dst + kMatBytes, d.kind ? &tm_do : &tm_v, d.h * 64, d.f0, bar);
+                const int boxes = d.rows > kTile ? 2 : 1;
+                mbar_arrive_expect_tx(bar, 2 * boxes * kBoxBytes);
+                for (int x = 0; x < boxes; ++x) {
+                    tma_load(dst + x * kBoxBytes, d.kind ? &tm_q : &tm_k, d.h * 64, d.f0 + x * kTile, bar);
+                    tma_load(dst + kMatBytes + x * kBoxBytes, d.kind ? &tm_do : &tm_v, d.h * 64, d.f0 + x * kTile, bar);
+                }
             }
             __syncwarp();
             ++nown;
-            for (int j = 0; j * kRows < d.T; ++j) {
+            for (int j = 0; j * kTile < d.T; ++j) {
                 const int s = nt % (int)kRing;
                 const uint32_t u = (uint32_t)(nt / (int)kRing);
                 if (u > 0 && !wait_bar(smem_u32(&bars->t_empty[s]), (u - 1) & 1, abort_flag, wait_ns, p.status)) {
@@ -396,10 +402,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (lane == 0) {
                     const uint32_t bar = smem_u32(&bars->t_full[s]);
-                    const uint32_t dst = ring_base + s * kPairBytes;
-                    mbar_arrive_expect_tx(bar, kPairBytes);
-                    tma_load(dst, d.kind ? &tm_k : &tm_q, d.h * 64, d.s0 + j * kRows, bar);
-                    tma_load(dst + kMatBytes, d.kind ? &tm_v : &tm_do, d.h * 64, d.s0 + j * kRows, bar);
+                    const uint32_t dst = ring_base + s * kStageBytes;
+                    mbar_arrive_expect_tx(bar, kStageBytes);
+                    tma_load(dst, d.kind ? &tm_k : &tm_q, d.h * 64, d.s0 + j * kTile, bar);
+                    tma_load(dst + kBoxBytes, d.kind ? &tm_v : &tm_do, d.h * 64, d.s0 + j * kTile, bar);
                 }
                 __syncwarp();
                 ++nt;
@@ -419,51 +425,50 @@ __global__ void __launch_bounds__(kThreads, 1)
                     wait_bar_drain(smem_u32(&bars->t_full[m % (int)kRing]), (uint32_t)(m / (int)kRing) & 1, wait_ns);
         }
         __syncwarp();
-    } else if (warp == 1) {
-        // ======================================================== S and D MMAs
+    } else if (warp == 1 || warp == 2) {
+        // ======================================================== S (warp 1) and D (warp 2) MMAs
+        const bool is_d = warp == 2;
         DescReader rd{0};
         ItemDesc d;
         uint32_t nt = 0, n = 0;
-        const uint64_t own0 = smem_desc_sw128(own_base, 16, 1024), ring0 = smem_desc_sw128(ring_base, 16, 1024);
+        const uint64_t own0 = smem_desc_sw128(own_base + (is_d ? kMatBytes : 0), 16, 1024);
+        const uint64_t ring0 = smem_desc_sw128(ring_base + (is_d ? kBoxBytes : 0), 16, 1024);
+        const uint32_t sh = is_d ? 1 : 2;   // D has one buffer a stream (two in all), S two (four)
+        uint64_t *full = is_d ? bars->d_full : bars->s_full, *empty = is_d ? bars->d_empty : bars->s_empty;
         bool ok = true;
         while (ok && rd.next(bars, p, abort_flag, d)) {
             const uint32_t os = n & 1;
             if (!wait_bar(smem_u32(&bars->own_full[os]), (n >> 1) & 1, abort_flag, wait_ns, p.status))
                 break;
             const uint64_t da = own0 + os * (kPairBytes >> 4);
-            for (int left = __shfl_sync(kFull, d.T, 0); left > 0; left -= kRows, ++nt) {
-                const uint32_t s = nt % kRing, b = nt & 1;
-                if (!wait_bar(smem_u32(&bars->t_ready[s]), (nt / kRing) & 1, abort_flag, wait_ns, p.status) ||
-                    (nt >= 2 &&
-                     !wait_bar(smem_u32(&bars->s_empty[b]), ((nt >> 1) - 1) & 1, abort_flag, wait_ns, p.status))) {
+            for (int left = __shfl_sync(kFull, d.T, 0); left > 0; left -= kTile, ++nt) {
+                const uint32_t s = nt % kRing, b = nt & ((1u << sh) - 1), u = nt >> sh;
+                if (!wait_bar(smem_u32(&bars->t_full[s]), (nt / kRing) & 1, abort_flag, wait_ns, p.status) ||
+                    (u > 0 && !wait_bar(smem_u32(&empty[b]), (u - 1) & 1, abort_flag, wait_ns, p.status))) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint64_t db = ring0 + s * (kPairBytes >> 4);
-                const uint32_t id = idesc_bf16_f32(128, left < kRows ? (left + 15) & ~15 : kRows, false);
-                const uint32_t ts = tmem + b * 128;
+                if (left < kTile && (left & 15)) {
+                    // rows past the segment up to the MMA's granule: their P
+                    // and dS are 0, but 0 * Inf would be NaN
+                    uint4 *z = reinterpret_cast<uint4 *>(smem + kRingOff + s * kStageBytes + (is_d ? kBoxBytes : 0) +
+                                                         left * kRowBytes);
+                    for (int i = lane; i < (16 - (left & 15)) * (kRowBytes / 16); i += 32)
+                        z[i] = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                const uint64_t db = ring0 + s * (kStageBytes >> 4);
+                const uint32_t id = idesc_bf16_f32(128, left < kTile ? (left + 15) & ~15 : kTile, false);
+                const uint32_t t = tmem + (nt & 1) * kStreamCols + (is_d ? kDCol : ((nt >> 1) & 1) * kTile);
                 // K steps of 16 elements = 32 bytes inside the 128-byte swizzle atom
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        mma_ss(ts, da + 2 * kk, db + 2 * kk, id, kk > 0 ? 1u : 0u);
-                    mma_commit(smem_u32(&bars->s_full[b]));
-                }
-                __syncwarp();
-                if (nt > 0 &&
-                    !wait_bar(smem_u32(&bars->d_empty), (nt - 1) & 1, abort_flag, wait_ns, p.status)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                if (elect_one()) {
-                    constexpr uint64_t kY = kMatBytes >> 4;   // from X, x to Y, y
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_ss(tmem + kDCol, da + kY + 2 * kk, db + kY + 2 * kk, id, kk > 0 ? 1u : 0u);
-                    mma_commit(smem_u32(&bars->d_full));
-                    if (left <= kRows)   // the item's last use of its owner tile
+                        mma_ss(t, da + 2 * kk, db + 2 * kk, id, kk > 0 ? 1u : 0u);
+                    mma_commit(smem_u32(&full[b]));
+                    if (left <= kTile)   // the item's last use of its owner matrix
                         mma_commit(smem_u32(&bars->own_empty[os]));
                 }
                 __syncwarp();
@@ -472,8 +477,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // every MMA must finish before TMEM is released
         if (elect_one()) {
-            mma_commit(smem_u32(&bars->mma_done[0]));
-            wait_bar_drain(smem_u32(&bars->mma_done[0]), 0, wait_ns);
+            mma_commit(smem_u32(&bars->mma_done[is_d]));
+            wait_bar_drain(smem_u32(&bars->mma_done[is_d]), 0, wait_ns);
         }
         __syncwarp();
     } else if (warp == 3) {
@@ -482,30 +487,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         ItemDesc d;
         uint32_t nt = 0, n = 0;
         const uint64_t ring0 = smem_desc_sw128(ring_base, 0, 1024);
-        const uint32_t id = idesc_bf16_f32(128, 64, true);
+        constexpr uint32_t id = idesc_bf16_f32(128, 64, true);
         bool ok = true;
         while (ok && rd.next(bars, p, abort_flag, d)) {
             const bool both = __shfl_sync(kFull, d.kind, 0) == 0;
             uint32_t acc = 0;
-            // the last item's accumulators have been read
+            // p_full of a tile speaks for one stream's warps only: the other's
+            // may still be reading the last item's accumulators
             if (n > 0 && !wait_bar(smem_u32(&bars->acc_empty), (n - 1) & 1, abort_flag, wait_ns, p.status))
                 break;
             ++n;
-            for (int left = __shfl_sync(kFull, d.T, 0); left > 0; left -= kRows, ++nt) {
-                const uint32_t s = nt % kRing, b = nt & 1;
-                if (!wait_bar(smem_u32(&bars->p_full[b]), (nt >> 1) & 1, abort_flag, wait_ns, p.status)) {
+            for (int left = __shfl_sync(kFull, d.T, 0); left > 0; left -= kTile, ++nt) {
+                const uint32_t s = nt % kRing, b = nt & 3;
+                if (!wait_bar(smem_u32(&bars->p_full[b]), (nt >> 2) & 1, abort_flag, wait_ns, p.status)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 // N = 64 is one 128-byte swizzle atom along N; K steps of 16
                 // rows advance the start by 2048 bytes
-                const uint64_t dx = ring0 + s * (kPairBytes >> 4), dy = dx + (kMatBytes >> 4);
-                const uint32_t a = tmem + b * 128;
-                const int steps = left < kRows ? (left + 15) >> 4 : kRows / 16;
+                const uint64_t dx = ring0 + s * (kStageBytes >> 4), dy = dx + (kBoxBytes >> 4);
+                const uint32_t a = tmem + (nt & 1) * kStreamCols + ((nt >> 1) & 1) * kTile;
+                const int steps = left < kTile ? (left + 15) >> 4 : kTile / 16;
                 if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < kRows / 16; ++kk) {
+                    for (int kk = 0; kk < kTile / 16; ++kk) {
                         if (kk < steps) {
                             const uint32_t ak = a + (kk >> 1) * kCols + (kk & 1) * 8;
                             const uint64_t row = (uint64_t)(kk * (16 * kRowBytes >> 4));
@@ -514,9 +520,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                             mma_ts(tmem + kAcc0, ak + kCols / 2, dx + row, id, kk ? 1u : acc);
                         }
                     }
-                    mma_commit(smem_u32(&bars->t_empty[s]));
                     mma_commit(smem_u32(&bars->s_empty[b]));
-                    if (left <= kRows)
+                    mma_commit(smem_u32(&bars->t_empty[s]));
+                    if (left <= kTile)
                         mma_commit(smem_u32(&bars->acc_full));
                 }
                 __syncwarp();
@@ -524,165 +530,102 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         if (elect_one()) {
-            mma_commit(smem_u32(&bars->mma_done[1]));
-            wait_bar_drain(smem_u32(&bars->mma_done[1]), 0, wait_ns);
+            mma_commit(smem_u32(&bars->mma_done[2]));
+            wait_bar_drain(smem_u32(&bars->mma_done[2]), 0, wait_ns);
         }
         __syncwarp();
-    } else if (warp == 2) {
-        // ======================================================== tile fix-up
+    } else if (warp >= kElem0) {
+        // ======================================================== elementwise
+        const int g = (warp - kElem0) >> 2;   // group: stream g >> 1, columns 32 (g & 1) .. + 31
+        const int stream = g >> 1, c0 = kCols * (g & 1);
+        const int qq = warp & 3;              // TMEM lane quarter of this warp
+        const uint32_t lanes = (uint32_t)(qq * 32) << 16;
+        const uint32_t tstream = tmem + stream * kStreamCols + c0 + lanes;
+        const int row = qq * 32 + lane;
+        float *cl = cols + (warp - kElem0) * (2 * kCols);
+        const uint32_t cl32 = smem_u32(cl);
         DescReader rd{0};
-        ItemDesc d;
-        int nt = 0;
-        bool ok = true;
-        while (ok && rd.next(bars, p, abort_flag, d)) {
-            for (int j = 0; j * kRows < d.T; ++j, ++nt) {
-                const int s = nt % (int)kRing;
-                const int nv = min(kRows, d.T - j * kRows);
-                const int nk = (nv + 15) & ~15;
-                float l[4], dl[4];
+        // lse and delta of an item: of this lane's row (kind 1), or of the
+        // lane's column in tile j (kind 0; nothing past the segment: P = 0)
+        auto fetch = [&](const ItemDesc &d, int j, float &l, float &dl) {
+            const int c = j * kTile + c0 + lane;
+            const bool in = d.kind ? row < d.rows : c < d.T;
+            const size_t at = (size_t)d.h * p.total + (d.kind ? d.f0 + row : d.s0 + c);
+            l = in ? __ldg(p.lse + at) : d.kind ? 0.f : INFINITY;
+            dl = in ? __ldg(p.delta + at) : 0.f;
+        };
+        ItemDesc d, dn;
+        int nt0 = 0, n = 0;   // the item's first tile; items
+        float vl = 0.f, vd = 0.f;
+        bool ok = rd.next(bars, p, abort_flag, d);
+        if (ok)
+            fetch(d, stream, vl, vd);
+        for (; ok; ++n) {
+            const bool active = qq * 32 < d.rows;   // warp-uniform
+            const int tiles = (d.T + kTile - 1) / kTile;
+            const float neg_lse2 = vl * -kLog2e, neg_delta = -vd;   // kind 1
+            // the stream's tiles of the item
+            for (int j = (nt0 ^ stream) & 1; j < tiles; j += 2) {
+                const int nt = nt0 + j, b = nt & 3;
+                const int valid = min(kTile, d.T - j * kTile) - c0;   // columns of this group in the segment
+                const uint32_t dpar = (uint32_t)(nt >> 1) & 1;
                 if (d.kind == 0) {
-                    const size_t at = (size_t)d.h * p.total + d.s0 + j * kRows;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int c = lane + 32 * i;
-                        l[i] = c < nv ? __ldg(p.lse + at + c) * -kLog2e : -INFINITY;
-                        dl[i] = c < nv ? -__ldg(p.delta + at + c) : 0.f;
-                    }
+                    // the columns' values, for the whole warp
+                    __syncwarp();
+                    cl[lane] = vl * -kLog2e;
+                    cl[kCols + lane] = -vd;
+                    __syncwarp();
+                    if (j + 2 < tiles)
+                        fetch(d, j + 2, vl, vd);
                 }
-                if (!wait_bar(smem_u32(&bars->t_full[s]), (uint32_t)(nt / (int)kRing) & 1, abort_flag, wait_ns, p.status)) {
+                if (!wait_bar(smem_u32(&bars->s_full[b]), ((uint32_t)nt >> 2) & 1, abort_flag, wait_ns, p.status)) {
                     ok = false;
                     break;
                 }
-                if (d.kind == 0) {
-                    float *cl = cols + s * (2 * kRows);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        cl[lane + 32 * i] = l[i];
-                        cl[kRows + lane + 32 * i] = dl[i];
-                    }
-                }
-                if (nv < nk) {
-                    for (int m = 0; m < 2; ++m) {
-                        uint4 *z = reinterpret_cast<uint4 *>(smem + kRingOff + s * kPairBytes + m * kMatBytes +
-                                                             nv * kRowBytes);
-                        for (int i = lane; i < (nk - nv) * (kRowBytes / 16); i += 32)
-                            z[i] = make_uint4(0, 0, 0, 0);
-                    }
-                    fence_proxy_async_smem();
-                }
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(smem_u32(&bars->t_ready[s]));
-            }
-        }
-    } else if (warp >= kElem0) {
-        // ======================================================== elementwise
-        const int g = (warp - kElem0) >> 2;   // warpgroup: columns 32g..32g+31
-        const int qq = warp & 3;              // TMEM lane quarter of this warp
-        const uint32_t lanes = (uint32_t)(qq * 32) << 16;
-        const int row = qq * 32 + lane;
-        // Items are read from the ring where they are needed (registers are
-        // scarce); an entry is released once its results are stored.
-        auto item = [&](uint32_t k) -> const volatile ItemDesc & { return bars->desc[k % kDescRing]; };
-        auto arrived = [&](uint32_t k) -> bool {   // item k is published and is not the end marker
-            return wait_bar(smem_u32(&bars->desc_full[k % kDescRing]), (k / kDescRing) & 1, abort_flag, wait_ns,
-                            p.status) &&
-                   item(k).rows >= 0;
-        };
-        // kind 1: lse and delta of this lane's row
-        auto fetch = [&](uint32_t k, float &l, float &dl) {
-            const bool in = item(k).kind == 1 && row < item(k).rows;
-            const size_t at = (size_t)item(k).h * p.total + item(k).f0 + row;
-            l = in ? __ldg(p.lse + at) : 0.f;
-            dl = in ? __ldg(p.delta + at) : 0.f;
-        };
-        uint32_t nt = 0, n = 0;   // tiles; the current item
-        float vl = 0.f, vd = 0.f;
-        bool have = arrived(0), ok = true, pending = false;
-        if (have)
-            fetch(0, vl, vd);
-        // One pass per item, and a last one that only stores.  An item's
-        // results are stored after the next one's first tile, so that its
-        // last MMAs run under that tile's arithmetic; the next item's row
-        // values travel while the item's last tile is computed.
-        for (;;) {
-            const bool active = have && qq * 32 < item(n).rows;   // warp-uniform
-            const bool kq = have && item(n).kind == 1;
-            const float neg_lse2 = vl * -kLog2e, neg_delta = -vd;
-            bool more = false;
-            for (int left = have ? item(n).T : 0;; left -= kRows) {
-                if (left > 0) {
-                    const uint32_t b = nt & 1, s = nt % kRing;
-                    const int valid = min(kRows, left) - kCols * g;   // columns of this warpgroup inside the segment
-                    // kind 0: the tile's lse and delta were staged before t_ready
-                    if ((!kq && !wait_bar(smem_u32(&bars->t_ready[s]), (nt / kRing) & 1, abort_flag, wait_ns,
-                                          p.status)) ||
-                        !wait_bar(smem_u32(&bars->s_full[b]), (nt >> 1) & 1, abort_flag, wait_ns, p.status)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    if (left <= kRows) {
-                        more = arrived(n + 1);
-                        if (more)
-                            fetch(n + 1, vl, vd);
-                    }
-                    if (active && valid > 0) {
-                        const uint32_t tS = tmem + b * 128 + kCols * g + lanes, tD = tmem + kDCol + kCols * g + lanes;
-                        const uint32_t cl = smem_u32(cols) + 4 * (s * (2 * kRows) + kCols * g);
-                        ok = kq ? elem_tile<true>(tS, tD, valid, p.scale_log2, neg_lse2, neg_delta, cl, bars, nt & 1, p,
-                                                  abort_flag)
-                                : elem_tile<false>(tS, tD, valid, p.scale_log2, neg_lse2, neg_delta, cl, bars, nt & 1,
-                                                   p, abort_flag);
-                    } else {
-                        ok = wait_bar(smem_u32(&bars->d_full), nt & 1, abort_flag, wait_ns, p.status);
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive(smem_u32(&bars->d_empty));
-                    }
-                    if (!ok)
-                        break;
-                    tc_fence_before();
+                tc_fence_after();
+                if (active && valid > 0) {
+                    const uint32_t tS = tstream + ((nt >> 1) & 1) * kTile, tD = tstream + kDCol;
+                    ok = d.kind ? elem_tile<true>(tS, tD, valid, p.scale_log2, neg_lse2, neg_delta, cl32,
+                                                  bars, stream, dpar, p, abort_flag)
+                                : elem_tile<false>(tS, tD, valid, p.scale_log2, neg_lse2, neg_delta, cl32,
+                                                   bars, stream, dpar, p, abort_flag);
+                } else {
+                    ok = wait_bar(smem_u32(&bars->d_full[stream]), dpar, abort_flag, wait_ns, p.status);
                     __syncwarp();
                     if (lane == 0)
-                        mbar_arrive(smem_u32(&bars->p_full[b]));
-                    ++nt;
+                        mbar_arrive(smem_u32(&bars->d_empty[stream]));
                 }
-                if (pending) {
-                    // ---------------------------------------------- output rows
-                    if (!wait_bar(smem_u32(&bars->acc_full), (n - 1) & 1, abort_flag, wait_ns, p.status)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    // kind 0: warpgroups 0, 1 store dK, 2, 3 dV; kind 1: 0, 1 store dQ
-                    const bool pq = item(n - 1).kind == 1;
-                    const int rows = item(n - 1).rows - qq * 32;
-                    const bool mine = rows > 0 && (!pq || g < 2);
-                    const int c = 32 * (g & 1);
-                    uint32_t o[16];
-                    if (mine)
-                        load_acc(tmem + (g < 2 ? kAcc0 : kAcc1) + c + lanes, g < 2 ? p.scale : 1.f, o);
-                    __nv_bfloat16 *dst = (pq ? p.dq : g < 2 ? p.dk : p.dv) +
-                                         (item(n - 1).f0 + qq * 32) * p.out_stride + item(n - 1).h * 64 + c;
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(smem_u32(&bars->acc_empty));
-                        mbar_arrive(smem_u32(&bars->desc_empty[(n - 1) % kDescRing]));
-                    }
-                    if (mine)
-                        store_rows(o, dst, p.out_stride, rows);
-                    pending = false;
-                }
-                if (left <= kRows)
+                if (!ok)
                     break;
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_u32(&bars->p_full[b]));
             }
-            if (!ok || !have)
+            if (!ok)
                 break;
-            pending = true;
-            ++n;
-            have = more;
+            nt0 += tiles;
+            // the next item's values travel while this one's output is stored
+            const bool have = rd.next(bars, p, abort_flag, dn);
+            if (have)
+                fetch(dn, (nt0 ^ stream) & 1, vl, vd);
+            // ---------------------------------------------- output rows
+            if (!wait_bar(smem_u32(&bars->acc_full), (uint32_t)n & 1, abort_flag, wait_ns, p.status))
+                break;
+            tc_fence_after();
+            if (active && (d.kind == 0 || g < 2)) {
+                const int c = 32 * (g & 1);
+                const long long at = (d.f0 + qq * 32) * p.out_stride + d.h * 64 + c;
+                uint32_t o[16];
+                load_acc(tmem + (g < 2 ? kAcc0 : kAcc1) + c + lanes, g < 2 ? p.scale : 1.f, o);
+                store_rows(o, (d.kind ? p.dq : g < 2 ? p.dk : p.dv) + at, p.out_stride, d.rows - qq * 32);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(smem_u32(&bars->acc_empty));
+            d = dn;
+            ok = have;
         }
     }
 
@@ -765,7 +708,7 @@ int launch_attn_bwd(const nle_attn_bwd_args *a, int block, void *stream)
     // an even grid: the two kinds of an owner tile are taken in the same round
     const int grid = (int)(items < (di.sm_count & ~1) ? items : (di.sm_count & ~1));
     // the kernel counts the tiles that a CTA walks in 32 bits
-    if ((items / grid + 1) * ((block ? block : a->total_frames) / kRows + 1) > 0x7fffffffLL)
+    if ((items / grid + 1) * ((block ? block : a->total_frames) / kTile + 1) > 0x7fffffffLL)
         return NLE_ERR_UNSUPPORTED;
 
     Params p{};
@@ -794,10 +737,10 @@ int launch_attn_bwd(const nle_attn_bwd_args *a, int block, void *stream)
 
     CUtensorMap tq, tk, tv, tdo;
     const uint64_t cols = (uint64_t)dense, rows = (uint64_t)a->total_frames;
-    if (!nle::encode_tmap_bf16_2d(&tq, a->q, cols, rows, stride, 64, kRows) ||
-        !nle::encode_tmap_bf16_2d(&tk, a->k, cols, rows, stride, 64, kRows) ||
-        !nle::encode_tmap_bf16_2d(&tv, a->v, cols, rows, stride, 64, kRows) ||
-        !nle::encode_tmap_bf16_2d(&tdo, a->dout, cols, rows, dense, 64, kRows))
+    if (!nle::encode_tmap_bf16_2d(&tq, a->q, cols, rows, stride, 64, kTile) ||
+        !nle::encode_tmap_bf16_2d(&tk, a->k, cols, rows, stride, 64, kTile) ||
+        !nle::encode_tmap_bf16_2d(&tv, a->v, cols, rows, stride, 64, kTile) ||
+        !nle::encode_tmap_bf16_2d(&tdo, a->dout, cols, rows, dense, 64, kTile))
         return NLE_ERR_CUDA;
     if (!nle::allow_max_dynamic_smem(reinterpret_cast<const void *>(attn_bwd_kernel), dev, di.smem_optin))
         return NLE_ERR_CUDA;
@@ -809,32 +752,6 @@ int launch_attn_bwd(const nle_attn_bwd_args *a, int block, void *stream)
         static_cast<float *>(a->workspace), p.total, a->heads);
     if (cudaGetLastError() != cudaSuccess)
         return NLE_ERR_CUDA;
-    const bool whole = block && !(a->flags & NLE_FLAG_SPLIT_ITEMS) && (a->flags & NLE_FLAG_WHOLE_ITEMS);
-    if (whole) {
-        nle::BlockBwdArgs b{};
-        b.q = a->q;
-        b.k = a->k;
-        b.v = a->v;
-        b.dout = a->dout;
-        b.lse = a->lse;
-        b.delta = p.delta;
-        b.dq = a->dq;
-        b.dk = a->dk;
-        b.dv = a->dv;
-        b.cu = a->cu_seqlens;
-        b.status = a->dev_status;
-        b.total = a->total_frames;
-        b.stride = stride;
-        b.dstride = dstride;
-        b.n_seq = a->n_seq;
-        b.heads = a->heads;
-        b.block = block;
-        b.scale = p.scale;
-        b.scale_log2 = p.scale_log2;
-        b.wait_ns = p.wait_ns;
-        b.flags = a->flags;
-        return nle::launch_block_bwd(b, di, dev, units * a->heads, st);
-    }
     attn_bwd_kernel<<<grid, kThreads, smem, st>>>(tq, tk, tv, tdo, p);
     return cudaGetLastError() == cudaSuccess ? NLE_OK : NLE_ERR_CUDA;
 }
