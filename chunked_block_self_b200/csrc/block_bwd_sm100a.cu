@@ -132,7 +132,7 @@ __device__ __forceinline__ bool unit_idle(Bars *bars, int g, int x, uint32_t use
 // queries' -lse log2e, and 256 floats on their -delta.  Keys past the block
 // (not row_ok) give dS = 0: dQ sums over all keys of the MMAs' 16-row granule.
 template <int NH>
-__device__ __forceinline__ bool unit_work(uint32_t tS, const float *cl, uint8_t *dst, int row, bool row_ok, Bars *bars,
+__device__ __forceinline__ bool unit_work(uint32_t tS, uint32_t cl, uint8_t *dst, int row, bool row_ok, Bars *bars,
                                           int g, int x, uint32_t use, uint32_t nx, const Params &p,
                                           volatile int *abort_flag)
 {
@@ -155,9 +155,10 @@ __device__ __forceinline__ bool unit_work(uint32_t tS, const float *cl, uint8_t 
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int q = 8 * h + i;
-            const float4 l = reinterpret_cast<const float4 *>(cl)[q];
-            const uint64_t y0 = fma2(pair(s[4 * q], s[4 * q + 1]), k2, pair(l.x, l.y));
-            const uint64_t y1 = fma2(pair(s[4 * q + 2], s[4 * q + 3]), k2, pair(l.z, l.w));
+            uint64_t l0, l1;
+            lds_pairs(cl + 16 * q, l0, l1);
+            const uint64_t y0 = fma2(pair(s[4 * q], s[4 * q + 1]), k2, l0);
+            const uint64_t y1 = fma2(pair(s[4 * q + 2], s[4 * q + 3]), k2, l1);
             float a, b;
             unpair(y0, a, b);
             a = ex2_approx(a);
@@ -169,6 +170,10 @@ __device__ __forceinline__ bool unit_work(uint32_t tS, const float *cl, uint8_t 
             b = ex2_approx(b);
             pr[2 * q + 1] = pair(a, b);
             pk[2 * i + 1] = pack_bf16x2(a, b);
+            if (i & 1) {
+                pair_fence(pr[2 * q]);
+                pair_fence(pr[2 * q + 1]);
+            }
         }
         tmem_st16p(tS + 16 * h, pk);
     }
@@ -198,9 +203,12 @@ __device__ __forceinline__ bool unit_work(uint32_t tS, const float *cl, uint8_t 
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int q = 2 * i + j, r = 8 * h + q;
-                const float4 l = reinterpret_cast<const float4 *>(cl + 256)[r];
-                const uint64_t g0 = mul2(pr[2 * r], add2(pair(d[4 * q], d[4 * q + 1]), pair(l.x, l.y)));
-                const uint64_t g1 = mul2(pr[2 * r + 1], add2(pair(d[4 * q + 2], d[4 * q + 3]), pair(l.z, l.w)));
+                uint64_t l0, l1;
+                lds_pairs(cl + 1024 + 16 * r, l0, l1);
+                uint64_t g0 = mul2(pr[2 * r], add2(pair(d[4 * q], d[4 * q + 1]), l0));
+                uint64_t g1 = mul2(pr[2 * r + 1], add2(pair(d[4 * q + 2], d[4 * q + 3]), l1));
+                pair_fence(g0);
+                pair_fence(g1);
                 float a, b;
                 unpair(g0, a, b);
                 pk[2 * j] = row_ok ? pack_bf16x2(a, b) : 0u;
@@ -353,6 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             const int L = __shfl_sync(kFull, d.L, 0);
             uint32_t at[kMats];
+#pragma unroll
             for (int m = 0; m < kMats; ++m) {
                 at[m] = base + slot * p.slot_bytes;
                 slot = slot + 1 == p.slots ? 0 : slot + 1;
@@ -412,6 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int L = __shfl_sync(kFull, d.L, 0);
             uint32_t at[kMats];
             const int slot0 = slot;
+#pragma unroll
             for (int m = 0; m < kMats; ++m) {
                 at[m] = base + slot * p.slot_bytes;
                 slot = slot + 1 == p.slots ? 0 : slot + 1;
@@ -552,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 ++n;
             }
-            const float *cl = cols + ((n - 1) & 1) * 512;
+            const uint32_t cl = smem_u32(cols) + ((n - 1) & 1) * 2048;
             const bool active = c * kKeys + qq * 32 < d.L;   // warp-uniform
             const bool row_ok = c * kKeys + row < d.L;
             bool ok = true;
@@ -566,8 +576,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t nx = u >> 1 ? nx1 : nx0;
                     uint8_t *dst = smem + p.ds_off + u * kChunkBytes + row * kRowBytes;
                     ok = !active ? unit_idle(bars, g, u >> 1, use, nx, p, abort_flag)
-                         : two   ? unit_work<2>(tS, cl + c0, dst, row, row_ok, bars, g, u >> 1, use, nx, p, abort_flag)
-                                 : unit_work<1>(tS, cl + c0, dst, row, row_ok, bars, g, u >> 1, use, nx, p, abort_flag);
+                         : two   ? unit_work<2>(tS, cl + 4 * c0, dst, row, row_ok, bars, g, u >> 1, use, nx, p, abort_flag)
+                                 : unit_work<1>(tS, cl + 4 * c0, dst, row, row_ok, bars, g, u >> 1, use, nx, p, abort_flag);
                     if (!ok)
                         break;
                     tc_fence_before();
@@ -588,11 +598,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int nk = pend.L - pend.c * kKeys - qq * 32, nq = pend.last ? pend.L - g * kKeys - qq * 32 : 0;
                     uint32_t a[2][16], b[2][16];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if (nk > 0)
-                            load_acc(tmem + (g ? kVAcc : kKAcc) + 32 * h + lanes, g ? 1.f : p.scale, a[h]);
-                        if (nq > 0)
-                            load_acc(tmem + kQAcc + 64 * g + 32 * h + lanes, p.scale, b[h]);
+                    for (int h = 0; h < 2; ++h) {   // rows that are not there are read too and stored by nothing
+                        load_acc(tmem + (g ? kVAcc : kKAcc) + 32 * h + lanes, g ? 1.f : p.scale, a[h]);
+                        load_acc(tmem + kQAcc + 64 * g + 32 * h + lanes, p.scale, b[h]);
                     }
                     tc_fence_before();
                     __syncwarp();
