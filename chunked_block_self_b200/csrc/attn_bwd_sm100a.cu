@@ -752,6 +752,32 @@ int launch_attn_bwd(const nle_attn_bwd_args *a, int block, void *stream)
         static_cast<float *>(a->workspace), p.total, a->heads);
     if (cudaGetLastError() != cudaSuccess)
         return NLE_ERR_CUDA;
+    const bool whole = block && !(a->flags & NLE_FLAG_SPLIT_ITEMS) && (a->flags & NLE_FLAG_WHOLE_ITEMS);
+    if (whole) {
+        nle::BlockBwdArgs b{};
+        b.q = a->q;
+        b.k = a->k;
+        b.v = a->v;
+        b.dout = a->dout;
+        b.lse = a->lse;
+        b.delta = p.delta;
+        b.dq = a->dq;
+        b.dk = a->dk;
+        b.dv = a->dv;
+        b.cu = a->cu_seqlens;
+        b.status = a->dev_status;
+        b.total = a->total_frames;
+        b.stride = stride;
+        b.dstride = dstride;
+        b.n_seq = a->n_seq;
+        b.heads = a->heads;
+        b.block = block;
+        b.scale = p.scale;
+        b.scale_log2 = p.scale_log2;
+        b.wait_ns = p.wait_ns;
+        b.flags = a->flags;
+        return nle::launch_block_bwd(b, di, dev, units * a->heads, st);
+    }
     attn_bwd_kernel<<<grid, kThreads, smem, st>>>(tq, tk, tv, tdo, p);
     return cudaGetLastError() == cudaSuccess ? NLE_OK : NLE_ERR_CUDA;
 }
