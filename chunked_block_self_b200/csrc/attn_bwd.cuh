@@ -17,20 +17,6 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const void *tmap, int32_t
                  : "memory");
 }
 
-// Register split between the warpgroups of a 640-thread CTA launched with 96
-// registers a thread (61,440): the service warpgroup keeps 64, each of the
-// four elementwise ones takes 104 (8,192 + 53,248 = 61,440).  Executed by
-// every warp of the warpgroup.
-__device__ __forceinline__ void service_regs()
-{
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-}
-
-__device__ __forceinline__ void elementwise_regs()
-{
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
-}
-
 // ---------------------------------------------------------------- packed fp32 pairs
 __device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi)
 {

@@ -16,21 +16,22 @@
 // dS is written once, as 64-query chunks of 128-byte rows (one key each),
 // 128-byte swizzled: a row-major operand for dK and a column-major one for dQ.
 //
-// One persistent CTA per SM, 12 warps (168 registers; 20 warps of 96 spilled,
-// and beside 210 KB of shared memory the spills live in L2: twice the time):
+// One persistent CTA per SM, 16 warps:
 //   warp 0   TMA producer: K, Q, V, dO of an item, one box each, into a ring
 //            of matrix slots; publishes the item's descriptor.
-//   warp 1   issues S and D.
+//   warp 1   issues S (one unit ahead) and D.
 //   warp 2   issues dV, dK and dQ.
 //   warp 3   owns TMEM; zeroes operand rows past the block (up to the MMAs'
 //            16-row granule: their P and dS are 0, but 0 * Inf would be NaN)
 //            and stages the block's lse and delta (+inf and 0 past it).
-//   warps 4-11  elementwise, two groups of four warps on alternate units
-//            (group g: S, D buffer g): a lane owns one key of the tile.  They
-//            also store the results: a key tile's after the first unit of the
-//            next, so that its last MMAs run under arithmetic.
-// TMEM (512 columns): S, D of group g at 128 g and 128 g + 64 (P over S's
-// first 32 columns), dQ_0, dQ_1 at 256 and 320, dK at 384, dV at 448.
+//   warps 4-7   results: a key tile's dK and dV, an item's dQ.
+//   warps 8-15  elementwise, two groups of four warps on alternate units
+//            (group g: S, D buffer g): a lane owns one key of the tile.
+// Registers are what this division is for: beside 200 KB of shared memory a
+// spill lives in L2, and 120 bytes of them a thread cost 40 % of the time.
+// TMEM (512 columns): S, D of group g at 128 g and 128 g + 64 (P over D's
+// first 32 columns, so that the group's next S need not wait for dV), dQ_0,
+// dQ_1 at 256 and 320, dK at 384, dV at 448.
 //
 // Every mbarrier wait is bounded; on expiry the CTA drains its copies and
 // MMAs in flight, frees TMEM and returns.
@@ -45,9 +46,10 @@ namespace {
 
 using namespace nle;
 
-constexpr int kElem0 = 4;                            // first elementwise warp
+constexpr int kEpi0 = 4;                             // first of four result warps
+constexpr int kElem0 = 8;                            // first elementwise warp
 constexpr int kElemWarps = 8;                        // two groups of four
-constexpr int kThreads = 32 * (kElem0 + kElemWarps); // 384
+constexpr int kThreads = 32 * (kElem0 + kElemWarps); // 512
 constexpr int kKeys = 128;                           // keys of a tile (MMA M)
 constexpr int kUnit = 64;                            // queries of a unit
 constexpr int kRowBytes = 128;                       // one frame of one head: 64 bf16
@@ -56,9 +58,22 @@ constexpr uint32_t kChunkBytes = kKeys * kRowBytes;  // dS of a unit: 128 keys x
 constexpr int kMaxSlots = 8;
 constexpr int kMats = 4;                             // K, Q, V, dO
 constexpr int kDescRing = 4;
-constexpr int kDescReaders = 3 + kElemWarps;         // both MMA, fix-up and elementwise warps
+constexpr int kDescReaders = 3 + 4 + kElemWarps;     // both MMA, check, result and elementwise warps
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kGroupCols = 128, kDCol = 64, kQAcc = 256, kKAcc = 384, kVAcc = 448;
+
+// Register split of the launch's 128 a thread (65,536 in all): 96 for the
+// service and the result warpgroup, 152 for each of the two elementwise ones
+// (63,488).  Executed by whole warpgroups, before they part into roles.
+__device__ __forceinline__ void few_regs()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+}
+
+__device__ __forceinline__ void more_regs()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+}
 
 struct ItemDesc {
     int f0, L, h;   // the block (L < 0: no further item)
@@ -70,12 +85,13 @@ struct Bars {
     uint64_t ready[2];              // by item: matrices checked, columns staged
     uint64_t cols_empty[2];         // kElemWarps arrivals: the item's columns are no longer read
     uint64_t s_full[2], d_full[2];  // by group
-    uint64_t d_empty[2];            // 4 arrivals: D has been read
+    uint64_t s_empty[2];            // 4 arrivals: S has been read
     uint64_t p_full[2];             // 4 arrivals: P and dS written
-    uint64_t p_empty[2];            // the unit's dV and dK MMAs have completed (P)
+    uint64_t p_empty[2];            // the unit's dV and dK MMAs have completed (P, over D)
     uint64_t dq_done[2];            // the key tile's dQ_x MMAs have completed (dS chunks 2x, 2x + 1)
     uint64_t acc_full;              // the key tile's sums (the item's, on its last) are complete
-    uint64_t acc_empty;             // kElemWarps arrivals: they have been read
+    uint64_t acc_empty;             // 4 arrivals: dK and dV have been read
+    uint64_t dq_empty;              // 4 arrivals: the item's dQ has been read
     uint64_t mma_done[2];
     uint64_t desc_full[kDescRing];
     uint64_t desc_empty[kDescRing];
@@ -118,16 +134,17 @@ struct DescReader {
 __device__ __forceinline__ bool unit_idle(Bars *bars, int g, int x, uint32_t use, uint32_t nx, const Params &p,
                                           volatile int *abort_flag)
 {
-    if (!wait_bar(smem_u32(&bars->s_full[g]), use & 1, abort_flag, p.wait_ns, p.status) ||
-        !wait_bar(smem_u32(&bars->d_full[g]), use & 1, abort_flag, p.wait_ns, p.status))
+    if (!wait_bar(smem_u32(&bars->s_full[g]), use & 1, abort_flag, p.wait_ns, p.status))
         return false;
     __syncwarp();
     if ((threadIdx.x & 31) == 0)
-        mbar_arrive(smem_u32(&bars->d_empty[g]));
+        mbar_arrive(smem_u32(&bars->s_empty[g]));
+    if (!wait_bar(smem_u32(&bars->d_full[g]), use & 1, abort_flag, p.wait_ns, p.status))
+        return false;
     return nx == 0 || wait_bar(smem_u32(&bars->dq_done[x]), (nx - 1) & 1, abort_flag, p.wait_ns, p.status);
 }
 
-// A unit for one lane (one key): P of its 32 * NH queries to TMEM over S, dS
+// A unit for one lane (one key): P of its 32 * NH queries to TMEM over D, dS
 // to the lane's row of the shared-memory chunk (128-byte swizzle).  cl: the
 // queries' -lse log2e, and 256 floats on their -delta.  Keys past the block
 // (not row_ok) give dS = 0: dQ sums over all keys of the MMAs' 16-row granule.
@@ -147,35 +164,27 @@ __device__ __forceinline__ bool unit_work(uint32_t tS, uint32_t cl, uint8_t *dst
 #pragma unroll
     for (int i = 0; i < 32 * NH; ++i)
         reg_fence(s[i]);
+    tc_fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0)
+        mbar_arrive(smem_u32(&bars->s_empty[g]));
     const uint64_t k2 = pair(p.scale_log2, p.scale_log2);
     uint64_t pr[16 * NH];
 #pragma unroll
-    for (int h = 0; h < NH; ++h) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int q = 8 * h + i;
-            uint64_t l0, l1;
-            lds_pairs(cl + 16 * q, l0, l1);
-            const uint64_t y0 = fma2(pair(s[4 * q], s[4 * q + 1]), k2, l0);
-            const uint64_t y1 = fma2(pair(s[4 * q + 2], s[4 * q + 3]), k2, l1);
-            float a, b;
-            unpair(y0, a, b);
-            a = ex2_approx(a);
-            b = ex2_approx(b);
-            pr[2 * q] = pair(a, b);
-            pk[2 * i] = pack_bf16x2(a, b);
-            unpair(y1, a, b);
-            a = ex2_approx(a);
-            b = ex2_approx(b);
-            pr[2 * q + 1] = pair(a, b);
-            pk[2 * i + 1] = pack_bf16x2(a, b);
-            if (i & 1) {
-                pair_fence(pr[2 * q]);
-                pair_fence(pr[2 * q + 1]);
-            }
+    for (int q = 0; q < 8 * NH; ++q) {
+        uint64_t l0, l1;
+        lds_pairs(cl + 16 * q, l0, l1);
+        const uint64_t y0 = fma2(pair(s[4 * q], s[4 * q + 1]), k2, l0);
+        const uint64_t y1 = fma2(pair(s[4 * q + 2], s[4 * q + 3]), k2, l1);
+        float a, b;
+        unpair(y0, a, b);
+        pr[2 * q] = pair(ex2_approx(a), ex2_approx(b));
+        unpair(y1, a, b);
+        pr[2 * q + 1] = pair(ex2_approx(a), ex2_approx(b));
+        if (q & 1) {   // at most two loads ahead of their use (registers)
+            pair_fence(pr[2 * q]);
+            pair_fence(pr[2 * q + 1]);
         }
-        tmem_st16p(tS + 16 * h, pk);
     }
     if (!wait_bar(smem_u32(&bars->d_full[g]), use & 1, abort_flag, p.wait_ns, p.status))
         return false;
@@ -191,11 +200,18 @@ __device__ __forceinline__ bool unit_work(uint32_t tS, uint32_t cl, uint8_t *dst
 #pragma unroll
         for (int i = 0; i < 32; ++i)
             reg_fence(d[i]);
-        if (h == NH - 1) {   // D has been read
-            tc_fence_before();
-            __syncwarp();
-            if ((threadIdx.x & 31) == 0)
-                mbar_arrive(smem_u32(&bars->d_empty[g]));
+        if (h == 0) {   // P over the half of D that is in registers
+#pragma unroll
+            for (int k = 0; k < NH; ++k) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    float a, b;
+                    unpair(pr[16 * k + i], a, b);
+                    pk[i] = pack_bf16x2(a, b);
+                }
+                tmem_st16p(tS + kDCol + 16 * k, pk);
+            }
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -223,13 +239,6 @@ __device__ __forceinline__ bool unit_work(uint32_t tS, uint32_t cl, uint8_t *dst
     return true;
 }
 
-// Results waiting to be stored: a key tile's dK, dV and, with its item's
-// last tile, the item's dQ.
-struct Pending {
-    int f0, L, h, c;
-    bool have, last;
-};
-
 __global__ void __launch_bounds__(kThreads, 1)
     block_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
@@ -255,14 +264,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&bars->cols_empty[g]), kElemWarps);
             mbar_init(smem_u32(&bars->s_full[g]), 1);
             mbar_init(smem_u32(&bars->d_full[g]), 1);
-            mbar_init(smem_u32(&bars->d_empty[g]), kElemWarps / 2);
+            mbar_init(smem_u32(&bars->s_empty[g]), kElemWarps / 2);
             mbar_init(smem_u32(&bars->p_full[g]), kElemWarps / 2);
             mbar_init(smem_u32(&bars->p_empty[g]), 1);
             mbar_init(smem_u32(&bars->dq_done[g]), 1);
             mbar_init(smem_u32(&bars->mma_done[g]), 1);
         }
         mbar_init(smem_u32(&bars->acc_full), 1);
-        mbar_init(smem_u32(&bars->acc_empty), kElemWarps);
+        mbar_init(smem_u32(&bars->acc_empty), 4);
+        mbar_init(smem_u32(&bars->dq_empty), 4);
         for (int j = 0; j < kDescRing; ++j) {
             mbar_init(smem_u32(&bars->desc_full[j]), 1);
             mbar_init(smem_u32(&bars->desc_empty[j]), kDescReaders);
@@ -290,6 +300,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         return wait_bar(smem_u32(bar), parity & 1, abort_flag, wait_ns, p.status);
     };
 
+    if (warp < kEpi0) {
+    few_regs();
     if (warp == 0) {
         // ======================================================== producer
         PlanWalker w;
@@ -368,13 +380,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const uint64_t dk0 = smem_desc_sw128(at[0], 16, 1024), dq0 = smem_desc_sw128(at[1], 16, 1024);
             const uint64_t dv0 = smem_desc_sw128(at[2], 16, 1024), do0 = smem_desc_sw128(at[3], 16, 1024);
-            for (int c = 0; ok && c * kKeys < L; ++c) {
-                for (int u = 0; u * kUnit < L; ++u, ++t) {
-                    const uint32_t g = t & 1, use = t >> 1;
-                    const uint32_t id = idesc_bf16_f32(128, min(kUnit, (L - u * kUnit + 15) & ~15), false);
-                    const uint32_t ts = tmem + g * kGroupCols;
-                    const uint64_t ca = (uint64_t)c * (kTileBytes >> 4), ub = (uint64_t)u * (kUnit * kRowBytes >> 4);
-                    if (use > 0 && !wait(&bars->p_empty[g], use - 1)) {
+            const int nu = (L + kUnit - 1) / kUnit, units = nu * ((L + kKeys - 1) / kKeys);
+            // S runs one unit ahead of D (inside the item: the next item's
+            // matrices may wait for this one's end)
+            int sc = 0, su = 0, dc = 0, du = 0;   // key tile and 64-query part of the next S and D
+            for (int i = 0; ok && i <= units; ++i) {
+                if (i < units) {
+                    const uint32_t g = (t + i) & 1, use = (t + i) >> 1;
+                    const uint32_t id = idesc_bf16_f32(128, min(kUnit, (L - su * kUnit + 15) & ~15), false);
+                    const uint64_t a = dk0 + sc * (kTileBytes >> 4), b = dq0 + su * (kUnit * kRowBytes >> 4);
+                    if (use > 0 && !wait(&bars->s_empty[g], use - 1)) {
                         ok = false;
                         break;
                     }
@@ -383,11 +398,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            mma_ss(ts, dk0 + ca + 2 * kk, dq0 + ub + 2 * kk, id, kk > 0 ? 1u : 0u);
+                            mma_ss(tmem + g * kGroupCols, a + 2 * kk, b + 2 * kk, id, kk > 0 ? 1u : 0u);
                         mma_commit(smem_u32(&bars->s_full[g]));
                     }
                     __syncwarp();
-                    if (use > 0 && !wait(&bars->d_empty[g], use - 1)) {
+                    if (++su == nu) {
+                        su = 0;
+                        ++sc;
+                    }
+                }
+                if (i > 0) {
+                    const uint32_t g = (t + i - 1) & 1, use = (t + i - 1) >> 1;
+                    const uint32_t id = idesc_bf16_f32(128, min(kUnit, (L - du * kUnit + 15) & ~15), false);
+                    const uint64_t a = dv0 + dc * (kTileBytes >> 4), b = do0 + du * (kUnit * kRowBytes >> 4);
+                    if (use > 0 && !wait(&bars->p_empty[g], use - 1)) {
                         ok = false;
                         break;
                     }
@@ -395,12 +419,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            mma_ss(ts + kDCol, dv0 + ca + 2 * kk, do0 + ub + 2 * kk, id, kk > 0 ? 1u : 0u);
+                            mma_ss(tmem + g * kGroupCols + kDCol, a + 2 * kk, b + 2 * kk, id, kk > 0 ? 1u : 0u);
                         mma_commit(smem_u32(&bars->d_full[g]));
                     }
                     __syncwarp();
+                    if (++du == nu) {
+                        du = 0;
+                        ++dc;
+                    }
                 }
             }
+            t += units;
             ++n;
         }
         // every MMA must finish before TMEM is released
@@ -413,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ======================================================== dV, dK and dQ MMAs
         DescReader rd{0};
         ItemDesc d;
-        uint32_t t = 0, kt = 0;   // units, key tiles
+        uint32_t t = 0, kt = 0, n = 0;   // units, key tiles, items
         int slot = 0;
         constexpr uint32_t id = idesc_bf16_f32(128, 64, true), id_q = id | (1u << 15);   // id_q: A is M-major too
         bool ok = true;
@@ -431,8 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t bk = smem_desc_sw128(at[0], 0, 1024), bq = smem_desc_sw128(at[1], 0, 1024);
             const uint64_t bo = smem_desc_sw128(at[3], 0, 1024);
             for (int c = 0; ok && c * kKeys < L; ++c, ++kt) {
-                // p_full speaks for one group: the other's warps may still be
-                // reading the last tile's sums
+                // the last tile's dK and dV have been read
                 if (kt > 0 && !wait(&bars->acc_empty, kt - 1)) {
                     ok = false;
                     break;
@@ -450,7 +478,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint64_t ub = (uint64_t)u * (kUnit * kRowBytes >> 4);
                     const uint64_t ak = smem_desc_sw128(ds_base + u * kChunkBytes, 16, 1024);
                     const bool last_u = (u + 1) * kUnit >= L;
-                    const uint32_t ap = tmem + g * kGroupCols;
+                    const uint32_t ap = tmem + g * kGroupCols + kDCol;
+                    // the item's first dQ: the last item's has been read
+                    if (c == 0 && (u == 1 || (u == 0 && last_u)) && n > 0 && !wait(&bars->dq_empty, n - 1)) {
+                        ok = false;
+                        break;
+                    }
                     if (elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk) {
@@ -483,13 +516,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                 }
             }
+            ++n;
         }
         if (elect_one()) {
             mma_commit(smem_u32(&bars->mma_done[1]));
             wait_bar_drain(smem_u32(&bars->mma_done[1]), 0, wait_ns);
         }
         __syncwarp();
-    } else if (warp == 3) {
+    } else {
         // ======================================================== operand check and columns
         DescReader rd{0};
         ItemDesc d;
@@ -533,43 +567,85 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             ++n;
         }
+    }
+    } else if (warp < kElem0) {
+        // ======================================================== results
+        few_regs();
+        const int qq = warp & 3;   // TMEM lane quarter of this warp
+        const uint32_t lanes = (uint32_t)(qq * 32) << 16;
+        DescReader rd{0};
+        ItemDesc d;
+        uint32_t kt = 0;   // key tiles
+        bool ok = true;
+        while (ok && rd.next(bars, p, abort_flag, d)) {
+            for (int c = 0; c * kKeys < d.L; ++c, ++kt) {
+                if (!wait(&bars->acc_full, kt)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                // rows that are not there are read too and stored by nothing
+                const int nk = d.L - c * kKeys - qq * 32;
+                const long long at = (long long)(d.f0 + c * kKeys + qq * 32) * p.out_stride + d.h * 64;
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    uint32_t o[2][16];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        load_acc(tmem + (m ? kVAcc : kKAcc) + 32 * h + lanes, m ? 1.f : p.scale, o[h]);
+                    if (m) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(smem_u32(&bars->acc_empty));
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        store_rows(o[h], (m ? p.dv : p.dk) + at + 32 * h, p.out_stride, nk);
+                }
+                if ((c + 1) * kKeys < d.L)
+                    continue;
+                // the item's last key tile: dQ
+                for (int x = 0; x * kKeys < d.L; ++x) {
+                    uint32_t o[2][16];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        load_acc(tmem + kQAcc + 64 * x + 32 * h + lanes, p.scale, o[h]);
+                    if ((x + 1) * kKeys >= d.L) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(smem_u32(&bars->dq_empty));
+                    }
+                    const long long aq = (long long)(d.f0 + x * kKeys + qq * 32) * p.out_stride + d.h * 64;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        store_rows(o[h], p.dq + aq + 32 * h, p.out_stride, d.L - x * kKeys - qq * 32);
+                }
+            }
+        }
     } else {
         // ======================================================== elementwise
-        const int e = warp - kElem0;
-        const int g = e >> 2;                        // group
+        more_regs();
+        const int g = (warp - kElem0) >> 2;          // group
         const int qq = warp & 3;                     // TMEM lane quarter of this warp
         const int row = qq * 32 + lane;              // key of the tile
         const uint32_t lanes = (uint32_t)(qq * 32) << 16;
         const uint32_t tS = tmem + g * kGroupCols + lanes;
         DescReader rd{0};
-        ItemDesc d{0, 0, 0};
-        uint32_t n = 0, t = 0, kt = 0;       // items and key tiles begun; units before the tile
+        ItemDesc d;
+        uint32_t n = 0, t = 0;               // items; units before the tile
         uint32_t nx0 = 0, nx1 = 0;           // key tiles that had queries in half 0, 1 of the block
-        int c = 0;                           // the item's current key tile
-        Pending pend{0, 0, 0, 0, false, false};
-        // One pass per key tile, and a last one that only stores.
-        for (;;) {
-            if (c * kKeys >= d.L) {   // the next item
-                if (n > 0) {
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(smem_u32(&bars->cols_empty[(n - 1) & 1]));
-                }
-                c = 0;
-                if (!rd.next(bars, p, abort_flag, d))
-                    d.L = 0;   // no further item (or a wait ran out: the next one returns at once)
-                else if (!wait(&bars->ready[n & 1], n >> 1))
-                    break;
-                ++n;
-            }
-            const uint32_t cl = smem_u32(cols) + ((n - 1) & 1) * 2048;
-            const bool active = c * kKeys + qq * 32 < d.L;   // warp-uniform
-            const bool row_ok = c * kKeys + row < d.L;
-            bool ok = true;
-            // the group's units of the tile
-            for (int u = (t ^ g) & 1;; u += 2) {
-                const bool have = u * kUnit < d.L;
-                if (have) {
+        bool ok = true;
+        for (; ok && rd.next(bars, p, abort_flag, d); ++n) {
+            if (!wait(&bars->ready[n & 1], n >> 1))
+                break;
+            const uint32_t cl = smem_u32(cols) + (n & 1) * 2048;
+            for (int c = 0; ok && c * kKeys < d.L; ++c) {
+                const bool active = c * kKeys + qq * 32 < d.L;   // warp-uniform
+                const bool row_ok = c * kKeys + row < d.L;
+                // the group's units of the tile
+                for (int u = (t ^ g) & 1; u * kUnit < d.L; u += 2) {
                     const uint32_t use = (t + u) >> 1;
                     const int c0 = u * kUnit;           // first query of the unit
                     const bool two = c0 + 32 < d.L;    // warp-uniform: queries in the unit's second half
@@ -585,48 +661,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0)
                         mbar_arrive(smem_u32(&bars->p_full[g]));
                 }
-                if (pend.have) {
-                    // the last key tile's results: dK by the first group, dV
-                    // by the second, and with an item's last tile dQ of
-                    // queries 128 g .. by group g
-                    pend.have = false;
-                    if (!wait(&bars->acc_full, kt - 1)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const int nk = pend.L - pend.c * kKeys - qq * 32, nq = pend.last ? pend.L - g * kKeys - qq * 32 : 0;
-                    uint32_t a[2][16], b[2][16];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {   // rows that are not there are read too and stored by nothing
-                        load_acc(tmem + (g ? kVAcc : kKAcc) + 32 * h + lanes, g ? 1.f : p.scale, a[h]);
-                        load_acc(tmem + kQAcc + 64 * g + 32 * h + lanes, p.scale, b[h]);
-                    }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(smem_u32(&bars->acc_empty));
-                    __nv_bfloat16 *da = (g ? p.dv : p.dk) + (pend.f0 + pend.c * kKeys + qq * 32) * p.out_stride + pend.h * 64;
-                    __nv_bfloat16 *db = p.dq + (pend.f0 + g * kKeys + qq * 32) * p.out_stride + pend.h * 64;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if (nk > 0)
-                            store_rows(a[h], da + 32 * h, p.out_stride, nk);
-                        if (nq > 0)
-                            store_rows(b[h], db + 32 * h, p.out_stride, nq);
-                    }
-                }
-                if (!have)
-                    break;
+                // a half without a unit for this group: its phase is waited for
+                // all the same (a parity wait only tells the phase before apart)
+                const int u0 = (t ^ g) & 1;
+                if (ok && ((u0 * kUnit >= d.L && nx0 > 0 && !wait(&bars->dq_done[0], nx0 - 1)) ||
+                           (d.L > kKeys && (2 + u0) * kUnit >= d.L && nx1 > 0 && !wait(&bars->dq_done[1], nx1 - 1))))
+                    ok = false;
+                t += (d.L + kUnit - 1) / kUnit;
+                ++nx0;
+                nx1 += d.L > kKeys;
             }
-            if (!ok || d.L == 0)
-                break;
-            t += (d.L + kUnit - 1) / kUnit;
-            ++nx0;
-            nx1 += d.L > kKeys;
-            pend = Pending{d.f0, d.L, d.h, c, true, (c + 1) * kKeys >= d.L};
-            ++kt;
-            ++c;
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(smem_u32(&bars->cols_empty[n & 1]));
         }
     }
 
