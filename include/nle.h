@@ -255,10 +255,17 @@ int nle_varlen_attn_fwd_ex(const void *q, const void *k, const void *v, void *ou
  *                heads * 64; a multiple of 8), so that they may lie inside
  *                one fused gradient buffer; frames of no utterance are not
  *                written.  They must not overlap any input.
- *   workspace    4 * heads * total_frames bytes of device scratch, 16-byte
- *                aligned, used by this call alone until it has run
+ *   workspace    4 * heads * total_frames bytes of device scratch, 4-byte
+ *                aligned, used by this call alone until it has run; its
+ *                content need not be kept
+ *   flags        NLE_FLAG_*; NLE_FLAG_WHOLE_ITEMS and NLE_FLAG_SPLIT_ITEMS
+ *                force a block gradient's work split (whole blocks on chip,
+ *                or 128-row tiles of either side; by default whole blocks
+ *                when block_frames is above 128 and there is a (block, head)
+ *                for every SM).  The two sum in different orders: each gives
+ *                the same bits on every call, not the bits of the other
  *   cu_seqlens, n_seq, total_frames, heads, d_head, softmax_scale,
- *   dev_status, flags, wait_limit_ns: as the forward's _ex form
+ *   dev_status, wait_limit_ns: as the forward's _ex form
  * block_frames must be the forward's (1..256).  q, k, v, out, dout, dq, dk
  * and dv are 16-byte aligned.  Two kernels on `stream`; no allocation.
  * Errors as for the forward entry points.

@@ -17,6 +17,10 @@ from oracle import attn_bwd, rope
 pytestmark = pytest.mark.gpu
 
 
+# (block length, 0: whole utterances; work split: 2 whole blocks on chip, 4 tiles)
+MODES = [(0, 0), (200, 2), (200, 4), (70, 2), (70, 4)]
+
+
 def _nle():
     from chunked_block_self_b200 import nle
     return nle
@@ -140,13 +144,13 @@ def test_workload_gradients_sampled_segments(cfg, block, cuda_device):
         _check_grads([g[a:a + n, h:h + 1] for g in grads], y, out[a:a + n, h:h + 1], [(0, n)])
 
 
-@pytest.mark.parametrize("block", [0, 70, 200])
-def test_gradient_locality_bit_exact(block, cuda_device):
+@pytest.mark.parametrize("block,flags", MODES)
+def test_gradient_locality_bit_exact(block, flags, cuda_device):
     """Poisoning every frame outside utterance 1 (Inf and NaN in q, k, v, dout,
     out and lse of its neighbours) leaves its gradients bit for bit."""
     x = _inputs([300, 450, 77], 2, 92)
     out, lse = _fwd(x, block)
-    ref = _bwd(x, block, out, lse)
+    ref = _bwd(x, block, out, lse, flags=flags)
     y = dict(x)
     for n in ("q", "k", "v", "dout"):
         y[n] = x[n].clone()
@@ -157,14 +161,14 @@ def test_gradient_locality_bit_exact(block, cuda_device):
     out2[750:] = float("inf")
     lse2[:, :300] = float("nan")
     lse2[:, 750:] = -float("inf")
-    got = _bwd(y, block, out2, lse2)
+    got = _bwd(y, block, out2, lse2, flags=flags)
     for a, b in zip(got, ref):
         assert torch.equal(a[300:750], b[300:750])
 
 
-@pytest.mark.parametrize("block", [0, 200])
+@pytest.mark.parametrize("block,flags", MODES)
 @pytest.mark.parametrize("sign", [1.0, -1.0])
-def test_extreme_scores(block, sign, cuda_device):
+def test_extreme_scores(block, flags, sign, cuda_device):
     """Scores of about +-200 in every valid place: exp of the masked places'
     score 0 relative to the row would overflow (-200) or vanish (+200)."""
     x = _inputs([137, 350], 2, 33, factor=0.05)
@@ -177,12 +181,12 @@ def test_extreme_scores(block, sign, cuda_device):
     ref = attn_bwd.backward(*(_np(x[n]) for n in ("dout", "q", "k", "v")), _np(out), segs, bounds=True,
                             # the exponent's error: 64 * 2^-24 * 200 of P, below 2^-10
                             rel=2.0 ** -8 + 2.0 ** -10)
-    for got, want, tol in zip(_bwd(x, block, out, lse), ref[:3], ref[3:]):
+    for got, want, tol in zip(_bwd(x, block, out, lse, flags=flags), ref[:3], ref[3:]):
         assert (np.abs(_np(got) - want) <= tol + 1e-30).all()
 
 
-@pytest.mark.parametrize("block", [0, 100])
-def test_peaked_rows(block, cuda_device):
+@pytest.mark.parametrize("block,flags", [(0, 0), (100, 4), (150, 2), (150, 4)])
+def test_peaked_rows(block, flags, cuda_device):
     """A few keys dominate: probabilities near one and near zero."""
     x = _inputs([260, 333], 2, 34)
     k = x["k"].float()
@@ -191,11 +195,11 @@ def test_peaked_rows(block, cuda_device):
     out, lse = _fwd(x, block)
     segs = attn_bwd.segments(x["cu"], block)
     _check_lse(lse, x, segs)
-    _check_grads(_bwd(x, block, out, lse), x, out, segs)
+    _check_grads(_bwd(x, block, out, lse, flags=flags), x, out, segs)
 
 
-@pytest.mark.parametrize("block", [0, 60])
-def test_projection_buffer_views_and_scale(block, cuda_device):
+@pytest.mark.parametrize("block,flags", [(0, 0), (60, 4), (130, 2)])
+def test_projection_buffer_views_and_scale(block, flags, cuda_device):
     """q, k, v inside one projection buffer, the gradients inside another, an
     explicit scale; rows of no utterance and the rest of the buffers stay."""
     x = _inputs([133, 45], 4, 95)
@@ -209,60 +213,61 @@ def test_projection_buffer_views_and_scale(block, cuda_device):
     out, lse = _fwd(y, block, softmax_scale=0.3)
     grads = torch.full((t, 3, 5, 64), 7.0, dtype=torch.bfloat16, device=cuda_device)
     views = (grads[:, 0, :4], grads[:, 1, :4], grads[:, 2, :4])
-    got = _bwd(y, block, out, lse, softmax_scale=0.3, grads=views)
+    got = _bwd(y, block, out, lse, softmax_scale=0.3, grads=views, flags=flags)
     assert all(a is b for a, b in zip(got, views))
     segs = attn_bwd.segments(x["cu"], block)
     _check_grads([g[20:198] for g in got], x, out[20:198], segs, scale=0.3)
     assert (grads[:20] == 7).all() and (grads[198:] == 7).all() and (grads[:, :, 4] == 7).all()
 
 
-@pytest.mark.parametrize("block", [0, 200])
-def test_empty_and_invalid_offsets(block, cuda_device):
+@pytest.mark.parametrize("block,flags", MODES[:3])
+def test_empty_and_invalid_offsets(block, flags, cuda_device):
     nle = _nle()
     x = _inputs([300, 100], 2, 96)
     out, lse = _fwd(x, block)
     for cu in (torch.zeros(3, dtype=torch.int32, device=cuda_device),
                torch.zeros(1, dtype=torch.int32, device=cuda_device)):
         grads = tuple(torch.full_like(x["q"], 5.0) for _ in range(3))
-        _bwd(dict(x, cud=cu), block, out, lse, grads=grads)
+        _bwd(dict(x, cud=cu), block, out, lse, grads=grads, flags=flags)
         assert all((g == 5).all() for g in grads)
     status = torch.zeros(1, dtype=torch.int32, device=cuda_device)
     grads = tuple(torch.full_like(x["q"], 5.0) for _ in range(3))
     bad = torch.tensor([0, 300, 900], dtype=torch.int32, device=cuda_device)   # beyond total
-    _bwd(dict(x, cud=bad), block, out, lse, grads=grads, dev_status=status)
+    _bwd(dict(x, cud=bad), block, out, lse, grads=grads, dev_status=status, flags=flags)
     assert int(status.item()) == nle.NLE_ERR_INVALID_ARG
-    ref = _bwd(x, block, out, lse)
+    ref = _bwd(x, block, out, lse, flags=flags)
     for g, r in zip(grads, ref):
         assert torch.equal(g[:300], r[:300]) and (g[300:] == 5).all()
     e = torch.empty(0, 2, 64, dtype=torch.bfloat16, device=cuda_device)
     z = dict(q=e, k=e, v=e, dout=e, cud=torch.zeros(2, dtype=torch.int32, device=cuda_device))
     eo, el = _fwd(z, block)
-    assert all(g.shape == (0, 2, 64) for g in _bwd(z, block, eo, el))
+    assert all(g.shape == (0, 2, 64) for g in _bwd(z, block, eo, el, flags=flags))
 
 
-@pytest.mark.parametrize("block", [0, 200])
-def test_timeout_path_reports_and_recovers(block, cuda_device):
+@pytest.mark.parametrize("block,flags", MODES[:3])
+def test_timeout_path_reports_and_recovers(block, flags, cuda_device):
     nle = _nle()
     x = _inputs([600, 300], 2, 97)
     out, lse = _fwd(x, block)
     status = torch.zeros(1, dtype=torch.int32, device=cuda_device)
-    _bwd(x, block, out, lse, dev_status=status, flags=nle.NLE_FLAG_TEST_SKIP_FIRST_LOAD, wait_limit_ns=2_000_000)
+    _bwd(x, block, out, lse, dev_status=status, flags=flags | nle.NLE_FLAG_TEST_SKIP_FIRST_LOAD,
+         wait_limit_ns=2_000_000)
     torch.cuda.synchronize()
     assert int(status.item()) == nle.NLE_ERR_TIMEOUT
-    _check_grads(_bwd(x, block, out, lse), x, out, attn_bwd.segments(x["cu"], block))
+    _check_grads(_bwd(x, block, out, lse, flags=flags), x, out, attn_bwd.segments(x["cu"], block))
 
 
-@pytest.mark.parametrize("block", [0, 200])
-def test_streams_and_graphs(block, cuda_device):
+@pytest.mark.parametrize("block,flags", MODES[:3])
+def test_streams_and_graphs(block, flags, cuda_device):
     """On a side stream; two captured graphs replayed in turn, each with its
     own scratch, on new values: the bits of plain calls."""
     x = _inputs([300, 741], 2, 98)
     out, lse = _fwd(x, block)
-    ref = [g.clone() for g in _bwd(x, block, out, lse)]
+    ref = [g.clone() for g in _bwd(x, block, out, lse, flags=flags)]
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     o2, l2 = _fwd(x, block, stream=side)
-    got = _bwd(x, block, o2, l2, stream=side)
+    got = _bwd(x, block, o2, l2, stream=side, flags=flags)
     side.synchronize()
     assert torch.equal(o2, out) and torch.equal(l2, lse)
     assert all(torch.equal(a, b) for a, b in zip(got, ref))
@@ -271,17 +276,74 @@ def test_streams_and_graphs(block, cuda_device):
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
             o, l = _fwd(x, block)
-            held.append(_bwd(x, block, o, l))
+            held.append(_bwd(x, block, o, l, flags=flags))
         graphs.append(g)
     x["v"].mul_(2)
     x["dout"].mul_(-0.5)
     out, lse = _fwd(x, block)
-    want = [g.clone() for g in _bwd(x, block, out, lse)]
+    want = [g.clone() for g in _bwd(x, block, out, lse, flags=flags)]
     for i in (0, 1, 0):
         graphs[i].replay()
     torch.cuda.synchronize()
     for h in held:
         assert all(torch.equal(a, b) for a, b in zip(h, want))
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_random_batches(seed, cuda_device):
+    """Random batches and block lengths (many items a CTA, one-frame blocks next
+    to full ones): every gradient against the definition, both splits."""
+    rng = np.random.default_rng(1000 + seed)
+    block = int(rng.integers(1, 257)) if seed % 2 else int(rng.integers(129, 257))
+    lengths = rng.integers(0, 3 * block, 90)
+    x = _inputs(lengths, 4, 2000 + seed)
+    out, lse = _fwd(x, block)
+    segs = attn_bwd.segments(x["cu"], block)
+    _check_grads(_bwd(x, block, out, lse, flags=2), x, out, segs)
+    _check_grads(_bwd(x, block, out, lse, flags=4), x, out, segs)
+
+
+def test_random_utterances(cuda_device):
+    """Many short utterances: items of one tile, so that one elementwise stream
+    of a CTA often has none."""
+    x = _inputs(np.random.default_rng(5).integers(0, 150, 120), 5, 3000)
+    out, lse = _fwd(x, 0)
+    _check_grads(_bwd(x, 0, out, lse), x, out, attn_bwd.segments(x["cu"]))
+
+
+@pytest.mark.parametrize("block,flags", [(0, 0), (150, 2), (150, 4)])
+def test_offsets_past_32_bits(block, flags, cuda_device):
+    """Frames so far apart that element offsets pass 2^31 and byte offsets
+    2^32: the bits of the dense call (2.2e9 elements of bf16, 4.4 GB a buffer)."""
+    x = _inputs([300, 33], 2, 77)
+    out, lse = _fwd(x, block)
+    ref = _bwd(x, block, out, lse, flags=flags)
+    stride = 6_600_000
+    wide = torch.empty(333 * stride, dtype=torch.bfloat16, device=cuda_device)
+    grads = torch.empty(333 * stride, dtype=torch.bfloat16, device=cuda_device)
+    views = [wide.as_strided((333, 2, 64), (stride, 64, 1), i * 128) for i in range(3)]
+    for v, n in zip(views, "qkv"):
+        v.copy_(x[n])
+    gviews = [grads.as_strided((333, 2, 64), (stride, 64, 1), i * 128) for i in range(3)]
+    y = dict(x, q=views[0], k=views[1], v=views[2])
+    o2, l2 = _fwd(y, block)
+    assert torch.equal(o2, out) and torch.equal(l2, lse)
+    got = _bwd(y, block, o2, l2, grads=gviews, flags=flags)
+    assert all(torch.equal(a, b) for a, b in zip(got, ref))
+
+
+def test_two_calls_at_once(cuda_device):
+    """Two gradients on two streams, interleaved: each has its own scratch."""
+    x, y = _inputs([900, 411], 3, 78), _inputs([511, 77, 640], 3, 79)
+    fx, fy = _fwd(x, 0), _fwd(y, 200)
+    rx, ry = _bwd(x, 0, *fx), _bwd(y, 200, *fy)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(5):
+        gx = _bwd(x, 0, *fx, stream=s1)
+        gy = _bwd(y, 200, *fy, stream=s2)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(gx + gy, rx + ry))
 
 
 def test_refused_tensors(cuda_device):

@@ -314,3 +314,40 @@ def test_other_stream_and_graph_replay(cuda_device):
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(held, want))
     assert not torch.equal(want[0], ref[0]) or not torch.equal(want[3], ref[3])
+
+
+def test_offsets_past_32_bits(cuda_device):
+    """Frames so far apart that element offsets pass 2^31: the bits of the
+    dense call, forward and gradient (2.2e9 elements of bf16, 4.4 GB)."""
+    nle = _nle()
+    x = _draw([300, 33], 2, 1, 21)
+    d = _dev(x, cuda_device)
+    ft = torch.from_numpy(_freq(64)).to(cuda_device)
+    ref = (*nle.qk_norm_rope(d["q"], d["k"], d["cu"], ft, d["wq"], d["wk"]),
+           *nle.qk_norm_rope_bwd(d["dq"], d["dk"], d["cu"], ft, d["q"], d["k"], d["wq"], d["wk"]))
+    stride = 6_600_000
+    wide = torch.empty(333 * stride, dtype=torch.bfloat16, device=cuda_device)
+    q, k, dq, dk = (wide.as_strided((333, h, 64), (stride, 64, 1), o * 64) for h, o in ((2, 0), (1, 2), (2, 3), (1, 5)))
+    for v, n in ((q, "q"), (k, "k"), (dq, "dq"), (dk, "dk")):
+        v.copy_(d[n])
+    _, _, gwq, gwk = nle.qk_norm_rope_bwd(dq, dk, d["cu"], ft, q, k, d["wq"], d["wk"], out=(dq, dk))
+    nle.qk_norm_rope(q, k, d["cu"], ft, d["wq"], d["wk"], out=(q, k))
+    assert all(torch.equal(a, b) for a, b in zip((q, k, dq, dk, gwq, gwk), ref))
+
+
+def test_heads_beyond_one_batch(cuda_device):
+    """More heads than a lane keeps in flight at once (16), not multiples of four."""
+    nle = _nle()
+    for inter in (False, True):
+        x = _draw([11], 37, 21, 22)
+        d = _dev(x, cuda_device)
+        f = _freq(48)
+        ft = torch.from_numpy(f).to(cuda_device)
+        qo, ko = nle.qk_norm_rope(d["q"], d["k"], d["cu"], ft, d["wq"], d["wk"], interleaved=inter)
+        gq, gk, gwq, gwk = nle.qk_norm_rope_bwd(d["dq"], d["dk"], d["cu"], ft, d["q"], d["k"], d["wq"], d["wk"],
+                                                interleaved=inter)
+        pos = rope.positions(x["cu"])
+        _check_fwd(qo, x["q"], x["wq"], pos, f, inter=inter)
+        _check_fwd(ko, x["k"], x["wk"], pos, f, inter=inter)
+        _check_bwd(gq, gwq, x["dq"], x["q"], x["wq"], pos, f, inter=inter)
+        _check_bwd(gk, gwk, x["dk"], x["k"], x["wk"], pos, f, inter=inter)
