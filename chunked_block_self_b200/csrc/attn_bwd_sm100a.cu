@@ -10,9 +10,9 @@
 //     dK_j  = s sum_i dS_ij q_i
 //
 // Two kinds of work item, each owning 128 rows of one head and walking the
-// segment's other side in tiles of 128, so that every sum stays in the
-// owner's TMEM accumulators: no atomics, no partial sums in memory, the same
-// bits every time.  With X, Y the owner's and x, y the tile's matrices:
+// segment's other side in tiles of 64, so that every sum stays in the owner's
+// TMEM accumulators: no atomics, no partial sums in memory, the same bits every
+// time.  With X, Y the owner's and x, y the tile's matrices:
 //   kind 0 (dK, dV): owner K, V (rows = keys), tiles Q, dO
 //     S = X x^T, D = Y y^T (both transposed: row = key, column = query),
 //     acc0 (dK) += dS x,  acc1 (dV) += P y
@@ -20,31 +20,38 @@
 //     S = X x^T, D = Y y^T,  acc0 (dQ) += dS x
 // P is formed twice (once per kind): 7 products of 2*64 FLOP and 2 exps per
 // (query, key) pair instead of 5 and 1, which costs less than the fp32
-// atomics (32 KB per 128 x 128 tile) that a single pass would add.
+// atomics (32 KB per 128 x 128 pairs) that a single pass would add.
 //
 // One persistent CTA per SM, 20 warps:
 //   warp 0   TMA producer: owner tiles (two stages), the segment's tiles into
-//            a ring; publishes every item's descriptor.
-//   warp 1   issues S and D (one elected lane): S of tile t + 1 runs while the
-//            elementwise warps work on tile t, D as soon as they have read t's.
-//   warp 2   tile fix-up: zeroes tile rows past the segment (up to the MMA's
-//            16-row granule: their P is 0, but 0 * Inf would be NaN) and, for
-//            kind 0, stages the tile's lse and delta (+inf and 0 past the
-//            segment, so that P and dS vanish there).
+//            a ring of eight; publishes every item's descriptor.
+//   warp 1   issues S, warp 2 issues D (one elected lane each), each after
+//            zeroing its operand's rows past the segment up to the MMA's
+//            16-row granule (their P and dS are 0, but 0 * Inf would be NaN).
 //   warp 3   owns TMEM and issues the accumulating MMAs (one elected lane).
-//   warps 4-19  elementwise, four warpgroups: every lane owns one row of the
-//            tile (its TMEM lane), warpgroup g the columns 32g..32g+31:
-//            P = exp2(S s log2e - lse log2e), dS = P (D - delta) in fp32, both
-//            rounded once to bf16 (the A operands of the accumulating MMAs)
-//            and written over S; then the output rows (acc times s, rounded
-//            to bf16, 16-byte stores of the segment's rows only).
-// The code of one tile is one short straight line per kind: the first form
-// (two warpgroups, 64 columns each, unrolled: about 40 KB of code walked per
-// tile) missed the instruction cache on 27 % of its requests, and the MMA
-// warp, idle in between, paid for each miss (4.2 k cycles a tile).
-// TMEM (512 columns): S buffers at 0 and 128 (after use: warpgroup g's P in
-// columns 32g..32g+15, its dS in 32g+16..32g+31), D at 256, acc0 at 384,
-// acc1 at 448.
+//   warps 4-19  elementwise, two streams of two warpgroups on alternate tiles:
+//            a lane owns one row of the tile (its TMEM lane), warpgroup g the
+//            columns 32 (g & 1) .. + 31.  P = exp2(S s log2e - lse log2e) and
+//            dS = P (D - delta) in fp32, each rounded once to bf16 (the A
+//            operands of the accumulating MMAs) and written over S.  lse and
+//            delta belong to the lane's row (kind 1), or to the columns
+//            (kind 0: fetched one tile ahead, +inf and 0 past the segment, so
+//            that P and dS vanish there).  At the end of an item the output
+//            rows: acc times s, rounded to bf16, the segment's rows only.
+// TMEM (512 columns): stream p at 192 p: two S buffers of 64 (after use: P of
+// the group's columns in its first 16, dS in its last 16), D at + 128; acc0 at
+// 384, acc1 at 448.
+//
+// What bounds it: the chain of a tile (S, read, exp, D, dS, write, accumulate)
+// takes about 2.4 k cycles, and two chains are in flight: about 1.2 k cycles a
+// tile, beside 512 for its 8192 exps and 512 (kind 1) or 640 (kind 0) for its
+// MMAs.  16 clips of 1950-4700 frames, 16 heads: 2.97 ms, 0.81 PFLOP/s over the
+// 7 products (0.49 of a measured bf16 GEMM), 0.58 over the formula's 5.  The
+// registers decide: 94 of the 96 that 640 threads leave, none spilled.  Beside
+// 200 KB of shared memory a spill lives in L2, and every form with more rows or
+// chains in flight that spilled was slower (three streams, decoupled buffers of
+// P and dS: 15 to 40 %).  Tiles of 128 rows in one chain of 32-column groups
+// come out alike on long clips and 3 to 15 % behind on blocks.
 //
 // Every mbarrier wait is bounded; on expiry the CTA drains its copies and
 // MMAs in flight, frees TMEM and returns.
@@ -92,7 +99,7 @@ struct Bars {
     uint64_t own_full[2];
     uint64_t own_empty[2];          // 2 arrivals: the item's last S and last D MMA have completed
     uint64_t t_full[kRing];
-    uint64_t t_empty[kRing];     // the tile's accumulating MMAs have completed
+    uint64_t t_empty[kRing];        // the tile's accumulating MMAs have completed
     uint64_t s_full[4];             // by tile & 3
     uint64_t s_empty[4];            // the accumulating MMAs that read P, dS have completed
     uint64_t p_full[4];             // kElemWarps / 2 arrivals: P and dS written
@@ -194,8 +201,8 @@ struct DescReader {
 
 // One tile for one lane: P and dS of the warpgroup's 32 columns, written over
 // its columns of S (P, kind 0 only, over the first 16, dS over the rest).
-// neg_lse2, neg_delta: -lse log2e and -delta, of the lane's row (kind 1) or,
-// from shared memory, of the columns (kind 0).  valid: columns inside the
+// neg_lse2, neg_delta: -lse log2e and -delta of the lane's row (kind 1); cl:
+// those of the columns, in shared memory (kind 0).  valid: columns inside the
 // segment; kind 1 masks the others by index (kind 0's have lse = +inf, so
 // P = 0, and zeroed operands, so D = 0).  False if the wait for D ran out.
 template <bool kDQ>
@@ -697,6 +704,14 @@ int launch_attn_bwd(const nle_attn_bwd_args *a, int block, void *stream)
     for (int i = 0; i < 8; ++i)
         if (!nle::aligned16(ptrs[i]))
             return NLE_ERR_MISALIGNED;
+    for (int i = 8; i < 11; ++i)
+        if (!nle::aligned4(ptrs[i]))
+            return NLE_ERR_MISALIGNED;
+    // what is written (dq, dk, dv, workspace) begins at no other buffer's start
+    for (int i = 5; i < 11; ++i)
+        for (int j = 0; j < i; ++j)
+            if (ptrs[i] == ptrs[j] && (i < 8 || i == 10 || j >= 5))
+                return NLE_ERR_INVALID_ARG;
 
     nle::DeviceInfo di;
     int dev = 0;

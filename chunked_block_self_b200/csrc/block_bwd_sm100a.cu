@@ -29,6 +29,12 @@
 //            (group g: S, D buffer g): a lane owns one key of the tile.
 // Registers are what this division is for: beside 200 KB of shared memory a
 // spill lives in L2, and 120 bytes of them a thread cost 40 % of the time.
+//
+// What bounds it: six 25 KB slots fit beside dS, so V and dO of the next
+// 200-frame block are loaded only when this one's products are done, about
+// 7 k of the 23 k cycles that an item takes; its eight units' chain (S, exp, D,
+// dS, accumulate) takes the rest, the exps 4 k, the products 5 k of it.  The
+// batch of 128 utterances (16 heads, blocks of 200): 0.40 ms without delta.
 // TMEM (512 columns): S, D of group g at 128 g and 128 g + 64 (P over D's
 // first 32 columns, so that the group's next S need not wait for dV), dQ_0,
 // dQ_1 at 256 and 320, dK at 384, dV at 448.
@@ -301,273 +307,273 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     if (warp < kEpi0) {
-    few_regs();
-    if (warp == 0) {
-        // ======================================================== producer
-        PlanWalker w;
-        w.init(p.cu, p.n_seq, p.total, p.block, lane);
-        const bool skip0 = (p.flags & NLE_FLAG_TEST_SKIP_FIRST_LOAD) != 0;
-        const uint64_t pol = policy_evict_first();   // every matrix is read once
-        const uint32_t bytes = (uint32_t)p.block * kRowBytes;
-        int n = 0;      // items published
-        int nm = 0;     // matrices claimed
-        bool stop = false;
-        auto publish = [&](const ItemDesc &d) -> bool {
-            const int j = n % kDescRing;
-            if (n >= kDescRing && !wait(&bars->desc_empty[j], (uint32_t)(n / kDescRing - 1)))
-                return false;
-            if (lane == 0) {
-                bars->desc[j] = d;
-                mbar_arrive(smem_u32(&bars->desc_full[j]));
-            }
-            __syncwarp();
-            ++n;
-            return true;
-        };
-        for (long long i = blockIdx.x; !stop; i += gridDim.x) {
-            ItemDesc d;
-            int seq;
-            const long long b = i / p.heads;
-            d.h = (int)(i - b * p.heads);
-            if (!w.find(b, lane, d.f0, d.L, seq))
-                break;
-            if (!publish(d)) {
-                stop = true;
-                break;
-            }
-            for (int m = 0; m < kMats; ++m) {
-                const int s = nm % p.slots, u = nm / p.slots;
-                if (u > 0 && !wait(&bars->m_empty[s], (uint32_t)(u - 1))) {
+        few_regs();
+        if (warp == 0) {
+            // ======================================================== producer
+            PlanWalker w;
+            w.init(p.cu, p.n_seq, p.total, p.block, lane);
+            const bool skip0 = (p.flags & NLE_FLAG_TEST_SKIP_FIRST_LOAD) != 0;
+            const uint64_t pol = policy_evict_first();   // every matrix is read once
+            const uint32_t bytes = (uint32_t)p.block * kRowBytes;
+            int n = 0;      // items published
+            int nm = 0;     // matrices claimed
+            bool stop = false;
+            auto publish = [&](const ItemDesc &d) -> bool {
+                const int j = n % kDescRing;
+                if (n >= kDescRing && !wait(&bars->desc_empty[j], (uint32_t)(n / kDescRing - 1)))
+                    return false;
+                if (lane == 0) {
+                    bars->desc[j] = d;
+                    mbar_arrive(smem_u32(&bars->desc_full[j]));
+                }
+                __syncwarp();
+                ++n;
+                return true;
+            };
+            for (long long i = blockIdx.x; !stop; i += gridDim.x) {
+                ItemDesc d;
+                int seq;
+                const long long b = i / p.heads;
+                d.h = (int)(i - b * p.heads);
+                if (!w.find(b, lane, d.f0, d.L, seq))
+                    break;
+                if (!publish(d)) {
                     stop = true;
                     break;
                 }
-                if (lane == 0 && !(skip0 && nm == 0)) {
-                    const uint32_t bar = smem_u32(&bars->m_full[s]);
-                    mbar_arrive_expect_tx(bar, bytes);
-                    tma_load_2d(base + s * p.slot_bytes, m == 0 ? &tm_k : m == 1 ? &tm_q : m == 2 ? &tm_v : &tm_do,
-                                d.h * 64, d.f0, bar, pol);
-                }
-                __syncwarp();
-                ++nm;
-            }
-        }
-        if (w.bad && lane == 0)
-            report(p.status, NLE_ERR_INVALID_ARG);
-        if (!stop)
-            publish(ItemDesc{0, -1, 0});
-        // drain: the last copy into each slot must land before exit
-        if (lane == 0)
-            for (int m = nm - p.slots; m < nm; ++m)
-                if (m >= 0 && !(skip0 && m == 0))
-                    wait_bar_drain(smem_u32(&bars->m_full[m % p.slots]), (uint32_t)(m / p.slots) & 1, wait_ns);
-        __syncwarp();
-    } else if (warp == 1) {
-        // ======================================================== S and D MMAs
-        DescReader rd{0};
-        ItemDesc d;
-        uint32_t n = 0, t = 0;   // items, units
-        int slot = 0;
-        bool ok = true;
-        while (ok && rd.next(bars, p, abort_flag, d)) {
-            if (!wait(&bars->ready[n & 1], n >> 1))
-                break;
-            const int L = __shfl_sync(kFull, d.L, 0);
-            uint32_t at[kMats];
-#pragma unroll
-            for (int m = 0; m < kMats; ++m) {
-                at[m] = base + slot * p.slot_bytes;
-                slot = slot + 1 == p.slots ? 0 : slot + 1;
-            }
-            const uint64_t dk0 = smem_desc_sw128(at[0], 16, 1024), dq0 = smem_desc_sw128(at[1], 16, 1024);
-            const uint64_t dv0 = smem_desc_sw128(at[2], 16, 1024), do0 = smem_desc_sw128(at[3], 16, 1024);
-            const int nu = (L + kUnit - 1) / kUnit, units = nu * ((L + kKeys - 1) / kKeys);
-            // S runs one unit ahead of D (inside the item: the next item's
-            // matrices may wait for this one's end)
-            int sc = 0, su = 0, dc = 0, du = 0;   // key tile and 64-query part of the next S and D
-            for (int i = 0; ok && i <= units; ++i) {
-                if (i < units) {
-                    const uint32_t g = (t + i) & 1, use = (t + i) >> 1;
-                    const uint32_t id = idesc_bf16_f32(128, min(kUnit, (L - su * kUnit + 15) & ~15), false);
-                    const uint64_t a = dk0 + sc * (kTileBytes >> 4), b = dq0 + su * (kUnit * kRowBytes >> 4);
-                    if (use > 0 && !wait(&bars->s_empty[g], use - 1)) {
-                        ok = false;
+                for (int m = 0; m < kMats; ++m) {
+                    const int s = nm % p.slots, u = nm / p.slots;
+                    if (u > 0 && !wait(&bars->m_empty[s], (uint32_t)(u - 1))) {
+                        stop = true;
                         break;
                     }
-                    tc_fence_after();
-                    // K steps of 16 elements = 32 bytes inside the 128-byte swizzle atom
-                    if (elect_one()) {
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma_ss(tmem + g * kGroupCols, a + 2 * kk, b + 2 * kk, id, kk > 0 ? 1u : 0u);
-                        mma_commit(smem_u32(&bars->s_full[g]));
+                    if (lane == 0 && !(skip0 && nm == 0)) {
+                        const uint32_t bar = smem_u32(&bars->m_full[s]);
+                        mbar_arrive_expect_tx(bar, bytes);
+                        tma_load_2d(base + s * p.slot_bytes, m == 0 ? &tm_k : m == 1 ? &tm_q : m == 2 ? &tm_v : &tm_do,
+                                    d.h * 64, d.f0, bar, pol);
                     }
                     __syncwarp();
-                    if (++su == nu) {
-                        su = 0;
-                        ++sc;
-                    }
-                }
-                if (i > 0) {
-                    const uint32_t g = (t + i - 1) & 1, use = (t + i - 1) >> 1;
-                    const uint32_t id = idesc_bf16_f32(128, min(kUnit, (L - du * kUnit + 15) & ~15), false);
-                    const uint64_t a = dv0 + dc * (kTileBytes >> 4), b = do0 + du * (kUnit * kRowBytes >> 4);
-                    if (use > 0 && !wait(&bars->p_empty[g], use - 1)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    if (elect_one()) {
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma_ss(tmem + g * kGroupCols + kDCol, a + 2 * kk, b + 2 * kk, id, kk > 0 ? 1u : 0u);
-                        mma_commit(smem_u32(&bars->d_full[g]));
-                    }
-                    __syncwarp();
-                    if (++du == nu) {
-                        du = 0;
-                        ++dc;
-                    }
+                    ++nm;
                 }
             }
-            t += units;
-            ++n;
-        }
-        // every MMA must finish before TMEM is released
-        if (elect_one()) {
-            mma_commit(smem_u32(&bars->mma_done[0]));
-            wait_bar_drain(smem_u32(&bars->mma_done[0]), 0, wait_ns);
-        }
-        __syncwarp();
-    } else if (warp == 2) {
-        // ======================================================== dV, dK and dQ MMAs
-        DescReader rd{0};
-        ItemDesc d;
-        uint32_t t = 0, kt = 0, n = 0;   // units, key tiles, items
-        int slot = 0;
-        constexpr uint32_t id = idesc_bf16_f32(128, 64, true), id_q = id | (1u << 15);   // id_q: A is M-major too
-        bool ok = true;
-        while (ok && rd.next(bars, p, abort_flag, d)) {
-            const int L = __shfl_sync(kFull, d.L, 0);
-            uint32_t at[kMats];
-            const int slot0 = slot;
-#pragma unroll
-            for (int m = 0; m < kMats; ++m) {
-                at[m] = base + slot * p.slot_bytes;
-                slot = slot + 1 == p.slots ? 0 : slot + 1;
-            }
-            // N = 64 is one 128-byte swizzle atom along N; K steps of 16 rows
-            // advance the start by 2048 bytes
-            const uint64_t bk = smem_desc_sw128(at[0], 0, 1024), bq = smem_desc_sw128(at[1], 0, 1024);
-            const uint64_t bo = smem_desc_sw128(at[3], 0, 1024);
-            for (int c = 0; ok && c * kKeys < L; ++c, ++kt) {
-                // the last tile's dK and dV have been read
-                if (kt > 0 && !wait(&bars->acc_empty, kt - 1)) {
-                    ok = false;
-                    break;
-                }
-                const int ksteps = (min(kKeys, L - c * kKeys) + 15) >> 4;
-                const bool last_c = (c + 1) * kKeys >= L;
-                for (int u = 0; u * kUnit < L; ++u, ++t) {
-                    const uint32_t g = t & 1;
-                    if (!wait(&bars->p_full[g], t >> 1)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const int steps = (min(kUnit, L - u * kUnit) + 15) >> 4;
-                    const uint64_t ub = (uint64_t)u * (kUnit * kRowBytes >> 4);
-                    const uint64_t ak = smem_desc_sw128(ds_base + u * kChunkBytes, 16, 1024);
-                    const bool last_u = (u + 1) * kUnit >= L;
-                    const uint32_t ap = tmem + g * kGroupCols + kDCol;
-                    // the item's first dQ: the last item's has been read
-                    if (c == 0 && (u == 1 || (u == 0 && last_u)) && n > 0 && !wait(&bars->dq_empty, n - 1)) {
-                        ok = false;
-                        break;
-                    }
-                    if (elect_one()) {
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk) {
-                            if (kk < steps) {
-                                const uint64_t row = ub + kk * (16 * kRowBytes >> 4);
-                                const uint32_t acc = u > 0 || kk > 0 ? 1u : 0u;
-                                mma_ts(tmem + kVAcc, ap + kk * 8, bo + row, id, acc);
-                                mma_ss(tmem + kKAcc, ak + 2 * kk, bq + row, id, acc);
-                            }
-                        }
-                        mma_commit(smem_u32(&bars->p_empty[g]));
-                        if ((u & 1) || last_u) {
-                            const int x = u >> 1;
-                            const uint64_t aq = smem_desc_sw128(ds_base + 2 * x * kChunkBytes, kChunkBytes, 1024);
-                            for (int kk = 0; kk < ksteps; ++kk) {
-                                const uint64_t row = kk * (16 * kRowBytes >> 4);
-                                mma_ss(tmem + kQAcc + 64 * x, aq + row, bk + (uint64_t)c * (kTileBytes >> 4) + row, id_q,
-                                       c > 0 || kk > 0 ? 1u : 0u);
-                            }
-                            mma_commit(smem_u32(&bars->dq_done[x]));
-                        }
-                        if (last_u) {
-                            mma_commit(smem_u32(&bars->acc_full));
-                            if (last_c)   // the item's matrices are free
-                                for (int m = 0; m < kMats; ++m)
-                                    mma_commit(smem_u32(&bars->m_empty[slot0 + m < p.slots ? slot0 + m
-                                                                                           : slot0 + m - p.slots]));
-                        }
-                    }
-                    __syncwarp();
-                }
-            }
-            ++n;
-        }
-        if (elect_one()) {
-            mma_commit(smem_u32(&bars->mma_done[1]));
-            wait_bar_drain(smem_u32(&bars->mma_done[1]), 0, wait_ns);
-        }
-        __syncwarp();
-    } else {
-        // ======================================================== operand check and columns
-        DescReader rd{0};
-        ItemDesc d;
-        uint32_t n = 0;
-        int nm = 0;
-        bool ok = true;
-        while (ok && rd.next(bars, p, abort_flag, d)) {
-            float l[8], dl[8];
-            const size_t at = (size_t)d.h * p.total + d.f0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int c = lane + 32 * i;
-                l[i] = c < d.L ? __ldg(p.lse + at + c) : INFINITY;
-                dl[i] = c < d.L ? __ldg(p.delta + at + c) : 0.f;
-            }
-            if (n >= 2 && !wait(&bars->cols_empty[n & 1], (n >> 1) - 1))
-                break;
-            float *cl = cols + (n & 1) * 512;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                cl[lane + 32 * i] = l[i] * -kLog2e;
-                cl[256 + lane + 32 * i] = -dl[i];
-            }
-            const int pad = -d.L & 15;
-            for (int m = 0; m < kMats; ++m, ++nm) {
-                const int s = nm % p.slots;
-                if (!wait(&bars->m_full[s], (uint32_t)(nm / p.slots))) {
-                    ok = false;
-                    break;
-                }
-                uint4 *z = reinterpret_cast<uint4 *>(smem + s * p.slot_bytes + d.L * kRowBytes);
-                for (int i = lane; i < pad * (kRowBytes / 16); i += 32)
-                    z[i] = make_uint4(0, 0, 0, 0);
-            }
-            if (!ok)
-                break;
-            fence_proxy_async_smem();
-            __syncwarp();
+            if (w.bad && lane == 0)
+                report(p.status, NLE_ERR_INVALID_ARG);
+            if (!stop)
+                publish(ItemDesc{0, -1, 0});
+            // drain: the last copy into each slot must land before exit
             if (lane == 0)
-                mbar_arrive(smem_u32(&bars->ready[n & 1]));
+                for (int m = nm - p.slots; m < nm; ++m)
+                    if (m >= 0 && !(skip0 && m == 0))
+                        wait_bar_drain(smem_u32(&bars->m_full[m % p.slots]), (uint32_t)(m / p.slots) & 1, wait_ns);
             __syncwarp();
-            ++n;
+        } else if (warp == 1) {
+            // ======================================================== S and D MMAs
+            DescReader rd{0};
+            ItemDesc d;
+            uint32_t n = 0, t = 0;   // items, units
+            int slot = 0;
+            bool ok = true;
+            while (ok && rd.next(bars, p, abort_flag, d)) {
+                if (!wait(&bars->ready[n & 1], n >> 1))
+                    break;
+                const int L = __shfl_sync(kFull, d.L, 0);
+                uint32_t at[kMats];
+    #pragma unroll
+                for (int m = 0; m < kMats; ++m) {
+                    at[m] = base + slot * p.slot_bytes;
+                    slot = slot + 1 == p.slots ? 0 : slot + 1;
+                }
+                const uint64_t dk0 = smem_desc_sw128(at[0], 16, 1024), dq0 = smem_desc_sw128(at[1], 16, 1024);
+                const uint64_t dv0 = smem_desc_sw128(at[2], 16, 1024), do0 = smem_desc_sw128(at[3], 16, 1024);
+                const int nu = (L + kUnit - 1) / kUnit, units = nu * ((L + kKeys - 1) / kKeys);
+                // S runs one unit ahead of D (inside the item: the next item's
+                // matrices may wait for this one's end)
+                int sc = 0, su = 0, dc = 0, du = 0;   // key tile and 64-query part of the next S and D
+                for (int i = 0; ok && i <= units; ++i) {
+                    if (i < units) {
+                        const uint32_t g = (t + i) & 1, use = (t + i) >> 1;
+                        const uint32_t id = idesc_bf16_f32(128, min(kUnit, (L - su * kUnit + 15) & ~15), false);
+                        const uint64_t a = dk0 + sc * (kTileBytes >> 4), b = dq0 + su * (kUnit * kRowBytes >> 4);
+                        if (use > 0 && !wait(&bars->s_empty[g], use - 1)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        // K steps of 16 elements = 32 bytes inside the 128-byte swizzle atom
+                        if (elect_one()) {
+    #pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                mma_ss(tmem + g * kGroupCols, a + 2 * kk, b + 2 * kk, id, kk > 0 ? 1u : 0u);
+                            mma_commit(smem_u32(&bars->s_full[g]));
+                        }
+                        __syncwarp();
+                        if (++su == nu) {
+                            su = 0;
+                            ++sc;
+                        }
+                    }
+                    if (i > 0) {
+                        const uint32_t g = (t + i - 1) & 1, use = (t + i - 1) >> 1;
+                        const uint32_t id = idesc_bf16_f32(128, min(kUnit, (L - du * kUnit + 15) & ~15), false);
+                        const uint64_t a = dv0 + dc * (kTileBytes >> 4), b = do0 + du * (kUnit * kRowBytes >> 4);
+                        if (use > 0 && !wait(&bars->p_empty[g], use - 1)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        if (elect_one()) {
+    #pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                mma_ss(tmem + g * kGroupCols + kDCol, a + 2 * kk, b + 2 * kk, id, kk > 0 ? 1u : 0u);
+                            mma_commit(smem_u32(&bars->d_full[g]));
+                        }
+                        __syncwarp();
+                        if (++du == nu) {
+                            du = 0;
+                            ++dc;
+                        }
+                    }
+                }
+                t += units;
+                ++n;
+            }
+            // every MMA must finish before TMEM is released
+            if (elect_one()) {
+                mma_commit(smem_u32(&bars->mma_done[0]));
+                wait_bar_drain(smem_u32(&bars->mma_done[0]), 0, wait_ns);
+            }
+            __syncwarp();
+        } else if (warp == 2) {
+            // ======================================================== dV, dK and dQ MMAs
+            DescReader rd{0};
+            ItemDesc d;
+            uint32_t t = 0, kt = 0, n = 0;   // units, key tiles, items
+            int slot = 0;
+            constexpr uint32_t id = idesc_bf16_f32(128, 64, true), id_q = id | (1u << 15);   // id_q: A is M-major too
+            bool ok = true;
+            while (ok && rd.next(bars, p, abort_flag, d)) {
+                const int L = __shfl_sync(kFull, d.L, 0);
+                uint32_t at[kMats];
+                const int slot0 = slot;
+    #pragma unroll
+                for (int m = 0; m < kMats; ++m) {
+                    at[m] = base + slot * p.slot_bytes;
+                    slot = slot + 1 == p.slots ? 0 : slot + 1;
+                }
+                // N = 64 is one 128-byte swizzle atom along N; K steps of 16 rows
+                // advance the start by 2048 bytes
+                const uint64_t bk = smem_desc_sw128(at[0], 0, 1024), bq = smem_desc_sw128(at[1], 0, 1024);
+                const uint64_t bo = smem_desc_sw128(at[3], 0, 1024);
+                for (int c = 0; ok && c * kKeys < L; ++c, ++kt) {
+                    // the last tile's dK and dV have been read
+                    if (kt > 0 && !wait(&bars->acc_empty, kt - 1)) {
+                        ok = false;
+                        break;
+                    }
+                    const int ksteps = (min(kKeys, L - c * kKeys) + 15) >> 4;
+                    const bool last_c = (c + 1) * kKeys >= L;
+                    for (int u = 0; u * kUnit < L; ++u, ++t) {
+                        const uint32_t g = t & 1;
+                        if (!wait(&bars->p_full[g], t >> 1)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const int steps = (min(kUnit, L - u * kUnit) + 15) >> 4;
+                        const uint64_t ub = (uint64_t)u * (kUnit * kRowBytes >> 4);
+                        const uint64_t ak = smem_desc_sw128(ds_base + u * kChunkBytes, 16, 1024);
+                        const bool last_u = (u + 1) * kUnit >= L;
+                        const uint32_t ap = tmem + g * kGroupCols + kDCol;
+                        // the item's first dQ: the last item's has been read
+                        if (c == 0 && (u == 1 || (u == 0 && last_u)) && n > 0 && !wait(&bars->dq_empty, n - 1)) {
+                            ok = false;
+                            break;
+                        }
+                        if (elect_one()) {
+    #pragma unroll
+                            for (int kk = 0; kk < 4; ++kk) {
+                                if (kk < steps) {
+                                    const uint64_t row = ub + kk * (16 * kRowBytes >> 4);
+                                    const uint32_t acc = u > 0 || kk > 0 ? 1u : 0u;
+                                    mma_ts(tmem + kVAcc, ap + kk * 8, bo + row, id, acc);
+                                    mma_ss(tmem + kKAcc, ak + 2 * kk, bq + row, id, acc);
+                                }
+                            }
+                            mma_commit(smem_u32(&bars->p_empty[g]));
+                            if ((u & 1) || last_u) {
+                                const int x = u >> 1;
+                                const uint64_t aq = smem_desc_sw128(ds_base + 2 * x * kChunkBytes, kChunkBytes, 1024);
+                                for (int kk = 0; kk < ksteps; ++kk) {
+                                    const uint64_t row = kk * (16 * kRowBytes >> 4);
+                                    mma_ss(tmem + kQAcc + 64 * x, aq + row, bk + c * (kTileBytes >> 4) + row, id_q,
+                                           c > 0 || kk > 0 ? 1u : 0u);
+                                }
+                                mma_commit(smem_u32(&bars->dq_done[x]));
+                            }
+                            if (last_u) {
+                                mma_commit(smem_u32(&bars->acc_full));
+                                if (last_c)   // the item's matrices are free
+                                    for (int m = 0; m < kMats; ++m)
+                                        mma_commit(smem_u32(&bars->m_empty[slot0 + m < p.slots ? slot0 + m
+                                                                                               : slot0 + m - p.slots]));
+                            }
+                        }
+                        __syncwarp();
+                    }
+                }
+                ++n;
+            }
+            if (elect_one()) {
+                mma_commit(smem_u32(&bars->mma_done[1]));
+                wait_bar_drain(smem_u32(&bars->mma_done[1]), 0, wait_ns);
+            }
+            __syncwarp();
+        } else {
+            // ======================================================== operand check and columns
+            DescReader rd{0};
+            ItemDesc d;
+            uint32_t n = 0;
+            int nm = 0;
+            bool ok = true;
+            while (ok && rd.next(bars, p, abort_flag, d)) {
+                float l[8], dl[8];
+                const size_t at = (size_t)d.h * p.total + d.f0;
+    #pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int c = lane + 32 * i;
+                    l[i] = c < d.L ? __ldg(p.lse + at + c) : INFINITY;
+                    dl[i] = c < d.L ? __ldg(p.delta + at + c) : 0.f;
+                }
+                if (n >= 2 && !wait(&bars->cols_empty[n & 1], (n >> 1) - 1))
+                    break;
+                float *cl = cols + (n & 1) * 512;
+    #pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    cl[lane + 32 * i] = l[i] * -kLog2e;
+                    cl[256 + lane + 32 * i] = -dl[i];
+                }
+                const int pad = -d.L & 15;
+                for (int m = 0; m < kMats; ++m, ++nm) {
+                    const int s = nm % p.slots;
+                    if (!wait(&bars->m_full[s], (uint32_t)(nm / p.slots))) {
+                        ok = false;
+                        break;
+                    }
+                    uint4 *z = reinterpret_cast<uint4 *>(smem + s * p.slot_bytes + d.L * kRowBytes);
+                    for (int i = lane; i < pad * (kRowBytes / 16); i += 32)
+                        z[i] = make_uint4(0, 0, 0, 0);
+                }
+                if (!ok)
+                    break;
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_u32(&bars->ready[n & 1]));
+                __syncwarp();
+                ++n;
+            }
         }
-    }
     } else if (warp < kElem0) {
         // ======================================================== results
         few_regs();
@@ -651,9 +657,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const bool two = c0 + 32 < d.L;    // warp-uniform: queries in the unit's second half
                     const uint32_t nx = u >> 1 ? nx1 : nx0;
                     uint8_t *dst = smem + p.ds_off + u * kChunkBytes + row * kRowBytes;
-                    ok = !active ? unit_idle(bars, g, u >> 1, use, nx, p, abort_flag)
-                         : two   ? unit_work<2>(tS, cl + 4 * c0, dst, row, row_ok, bars, g, u >> 1, use, nx, p, abort_flag)
-                                 : unit_work<1>(tS, cl + 4 * c0, dst, row, row_ok, bars, g, u >> 1, use, nx, p, abort_flag);
+                    const uint32_t uc = cl + 4 * c0;
+                    const int x = u >> 1;
+                    ok = !active ? unit_idle(bars, g, x, use, nx, p, abort_flag)
+                         : two   ? unit_work<2>(tS, uc, dst, row, row_ok, bars, g, x, use, nx, p, abort_flag)
+                                 : unit_work<1>(tS, uc, dst, row, row_ok, bars, g, x, use, nx, p, abort_flag);
                     if (!ok)
                         break;
                     tc_fence_before();

@@ -37,5 +37,6 @@ bool encode_tmap_bf16_heads(CUtensorMap *map, const void *base, uint64_t rows, u
 bool allow_max_dynamic_smem(const void *fn, int device, int smem_optin);
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 } // namespace nle

@@ -476,6 +476,9 @@ int check_plan(const nle_rope_plan *r, bool *work)
         return NLE_ERR_INVALID_ARG;
     if ((r->q_weight && !nle::aligned16(r->q_weight)) || (r->k_weight && !nle::aligned16(r->k_weight)))
         return NLE_ERR_MISALIGNED;
+    if (!nle::aligned4(r->cu_seqlens) || !nle::aligned4(r->positions) ||
+        (r->rot_dim > 0 && (reinterpret_cast<uintptr_t>(r->inv_freq) & 7)))
+        return NLE_ERR_MISALIGNED;
     *work = true;
     return NLE_OK;
 }
@@ -552,6 +555,8 @@ extern "C" int nle_qk_norm_rope_fwd(const nle_rope_plan *plan, const void *q, in
         if ((rc = check_rows(t[i].src, &t[i].ss, t[i].heads)) != NLE_OK ||
             (rc = check_rows(t[i].dst, &t[i].ds, t[i].heads)) != NLE_OK)
             return rc;
+        if (t[i].src == t[i].dst && t[i].ss != t[i].ds)   // in place: the same frames
+            return NLE_ERR_INVALID_ARG;
         Rows &r = i ? p.k : p.q;
         r.src = static_cast<const uint8_t *>(t[i].src);
         r.dst = static_cast<uint8_t *>(t[i].dst);
@@ -606,6 +611,8 @@ extern "C" int nle_qk_norm_rope_bwd(const nle_rope_plan *plan, const void *dq_ou
             (norm && (rc = check_rows(t[i].x, &t[i].xs, t[i].heads)) != NLE_OK) ||
             (rc = check_rows(t[i].dst, &t[i].ds, t[i].heads)) != NLE_OK)
             return rc;
+        if (t[i].src == t[i].dst && t[i].ss != t[i].ds)   // in place: the same frames
+            return NLE_ERR_INVALID_ARG;
         Rows &r = i ? p.k : p.q;
         r.src = static_cast<const uint8_t *>(t[i].src);
         r.x = static_cast<const uint8_t *>(t[i].x);

@@ -267,8 +267,9 @@ int nle_varlen_attn_fwd_ex(const void *q, const void *k, const void *v, void *ou
  *   cu_seqlens, n_seq, total_frames, heads, d_head, softmax_scale,
  *   dev_status, wait_limit_ns: as the forward's _ex form
  * block_frames must be the forward's (1..256).  q, k, v, out, dout, dq, dk
- * and dv are 16-byte aligned.  Two kernels on `stream`; no allocation.
- * Errors as for the forward entry points.
+ * and dv are 16-byte aligned, the rest 4-byte.  Two kernels on `stream`; no
+ * allocation.  Errors as for the forward entry points; NLE_ERR_INVALID_ARG
+ * also for a dq, dk, dv or workspace that begins where another buffer does.
  */
 int nle_block_attn_fwd_lse(const void *q, const void *k, const void *v, void *out, float *lse,
                            const int32_t *cu_seqlens, int n_seq, int64_t total_frames, int heads, int d_head,
@@ -320,7 +321,8 @@ int nle_varlen_attn_bwd(const nle_attn_bwd_args *args, void *stream);
  *   d_head       must be 64
  *   q_weight, k_weight  bf16 [64], 16-byte aligned; both NULL: no norm
  *   eps          >= 0
- *   inv_freq     double [rot_dim / 2] (may be NULL when rot_dim is 0)
+ *   inv_freq     double [rot_dim / 2], 8-byte aligned (may be NULL when
+ *                rot_dim is 0)
  *   rot_dim      0, 16, 32, 48 or 64
  *   interleaved  0 or 1
  *   rot_scale    0 selects 1

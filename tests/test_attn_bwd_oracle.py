@@ -101,7 +101,21 @@ def test_backward_host_refusals(f):
         assert f(**{n: None}) == inv, n
     for n in ("q", "k", "v", "out", "dout", "dq", "dk", "dv"):
         assert f(**{n: 24}) == mis, n
+    for n in ("lse", "cu_seqlens", "workspace"):
+        assert f(**{n: 18}) == mis, n
     assert f(n_seq=0, q=None) == nle.NLE_OK and f(total_frames=0, q=None) == nle.NLE_OK
+
+
+@pytest.mark.parametrize("f", [_block, _varlen])
+def test_outputs_that_begin_at_another_buffer(f):
+    """Only outputs that begin at an input, at another output or at the
+    workspace are refused; without them the call gets as far as the device."""
+    names = ("q", "k", "v", "out", "dout", "lse", "cu_seqlens", "dq", "dk", "dv", "workspace")
+    a = {n: 1024 * (i + 1) for i, n in enumerate(names)}
+    for n in ("dq", "dk", "dv", "workspace"):
+        for m in names:
+            if m != n:
+                assert f(**dict(a, **{n: a[m]})) == nle.NLE_ERR_INVALID_ARG, (n, m)
 
 
 def test_block_and_forward_host_refusals():
@@ -113,9 +127,11 @@ def test_block_and_forward_host_refusals():
     assert f(16, 16, 16, 16, None, 16, 1, 400, 8, 64, 200, 0.0, 0, None, 0, 0, None) == nle.NLE_ERR_INVALID_ARG
     assert f(16, 16, 16, 16, 16, 16, 1, 400, 8, 32, 200, 0.0, 0, None, 0, 0, None) == nle.NLE_ERR_UNSUPPORTED
     assert f(16, 16, 16, 16, None, 16, 0, 400, 8, 64, 200, 0.0, 0, None, 0, 0, None) == nle.NLE_OK
+    assert f(16, 16, 16, 16, 18, 16, 1, 400, 8, 64, 200, 0.0, 0, None, 0, 0, None) == nle.NLE_ERR_MISALIGNED
     f = nle._lib.nle_varlen_attn_fwd_lse
     assert f(16, 16, 16, 16, None, 16, 1, 400, 8, 64, 0.0, 0, None, 0, 0, None) == nle.NLE_ERR_INVALID_ARG
     assert f(16, 16, 16, 24, 16, 16, 1, 400, 8, 64, 0.0, 0, None, 0, 0, None) == nle.NLE_ERR_MISALIGNED
+    assert f(16, 16, 16, 16, 18, 16, 1, 400, 8, 64, 0.0, 0, None, 0, 0, None) == nle.NLE_ERR_MISALIGNED
 
 
 def test_binding_rejects_cpu_tensors():

@@ -119,13 +119,15 @@ def test_host_refusals(f):
                      (dict(eps=float("nan")), inv), (dict(interleaved=2), inv), (dict(inv_freq=None), inv),
                      (dict(cu_seqlens=None), inv), (dict(q_weight=None), inv), (dict(k_weight=None), inv),
                      (dict(q_weight=8), mis), (dict(q=None), inv), (dict(k=None), inv), (dict(q=8), mis),
-                     (dict(qs=8 * 64 - 8), inv), (dict(qs=8 * 64 + 4), mis), (dict(qs=1 << 41), inv)]:
+                     (dict(qs=8 * 64 - 8), inv), (dict(qs=8 * 64 + 4), mis), (dict(qs=1 << 41), inv),
+                     (dict(cu_seqlens=18), mis), (dict(positions=18), mis), (dict(inv_freq=20), mis)]:
         assert f(**kw) == want, kw
     # nothing to do: no pointer is looked at
     assert f(n_seq=0, q=None) == nle.NLE_OK
     if f is _fwd:
         assert f(total_frames=0, q=None) == nle.NLE_OK
         assert f(qo=None) == inv and f(ko=24) == mis
+        assert f(qs=9 * 64) == inv   # in place with another stride
         assert nle._lib.nle_qk_norm_rope_fwd(None, 16, 0, 16, 0, 16, 0, 16, 0, None) == inv
     else:
         assert f(dq=None) == inv and f(oq=None) == inv and f(work=None) == inv and f(work=24) == mis
