@@ -62,24 +62,12 @@ constexpr int kRowBytes = 128;                       // one frame of one head: 6
 constexpr uint32_t kTileBytes = kKeys * kRowBytes;   // 16 KB
 constexpr uint32_t kChunkBytes = kKeys * kRowBytes;  // dS of a unit: 128 keys x 64 queries
 constexpr int kMaxSlots = 8;
-constexpr int kMats = 4;                             // K, Q, V, dO
+constexpr int kMats = 4;
+enum { kMatK, kMatQ, kMatO, kMatV };                 // O: dO
 constexpr int kDescRing = 4;
 constexpr int kDescReaders = 3 + 4 + kElemWarps;     // both MMA, check, result and elementwise warps
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kGroupCols = 128, kDCol = 64, kQAcc = 256, kKAcc = 384, kVAcc = 448;
-
-// Register split of the launch's 128 a thread (65,536 in all): 96 for the
-// service and the result warpgroup, 152 for each of the two elementwise ones
-// (63,488).  Executed by whole warpgroups, before they part into roles.
-__device__ __forceinline__ void few_regs()
-{
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
-}
-
-__device__ __forceinline__ void more_regs()
-{
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
-}
 
 struct ItemDesc {
     int f0, L, h;   // the block (L < 0: no further item)
@@ -87,14 +75,16 @@ struct ItemDesc {
 
 struct Bars {
     uint64_t m_full[kMaxSlots];
-    uint64_t m_empty[kMaxSlots];    // the item's last MMAs have completed
-    uint64_t ready[2];              // by item: matrices checked, columns staged
+    uint64_t m_empty[kMaxSlots];    // the item's last MMAs on the matrix have completed
+    uint64_t ready_s[2];            // by item: K and Q checked, columns staged
+    uint64_t ready_d[2];            // by item: V and dO checked
     uint64_t cols_empty[2];         // kElemWarps arrivals: the item's columns are no longer read
     uint64_t s_full[2], d_full[2];  // by group
     uint64_t s_empty[2];            // 4 arrivals: S has been read
     uint64_t p_full[2];             // 4 arrivals: P and dS written
     uint64_t p_empty[2];            // the unit's dV and dK MMAs have completed (P, over D)
     uint64_t dq_done[2];            // the key tile's dQ_x MMAs have completed (dS chunks 2x, 2x + 1)
+    uint64_t idle;                  // 4 arrivals: the group without a unit in an item of one unit
     uint64_t acc_full;              // the key tile's sums (the item's, on its last) are complete
     uint64_t acc_empty;             // 4 arrivals: dK and dV have been read
     uint64_t dq_empty;              // 4 arrivals: the item's dQ has been read
@@ -118,6 +108,18 @@ struct Params {
     int32_t *status;
     unsigned long long wait_ns;
     int flags;
+};
+
+// Matrix m of item n: the first slots - 4 of K, Q, dO, V have two slots each.
+struct Slot {
+    int at, use;   // slot; how often it was used before
+    __device__ __forceinline__ Slot(int m, int n, int slots)
+    {
+        const int two = slots - kMats;
+        const bool twice = m < two;
+        at = m + min(m, two) + (twice ? n & 1 : 0);
+        use = twice ? n >> 1 : n;
+    }
 };
 
 struct DescReader {
@@ -150,94 +152,85 @@ __device__ __forceinline__ bool unit_idle(Bars *bars, int g, int x, uint32_t use
     return nx == 0 || wait_bar(smem_u32(&bars->dq_done[x]), (nx - 1) & 1, abort_flag, p.wait_ns, p.status);
 }
 
-// A unit for one lane (one key): P of its 32 * NH queries to TMEM over D, dS
-// to the lane's row of the shared-memory chunk (128-byte swizzle).  cl: the
-// queries' -lse log2e, and 256 floats on their -delta.  Keys past the block
-// (not row_ok) give dS = 0: dQ sums over all keys of the MMAs' 16-row granule.
-template <int NH>
-__device__ __forceinline__ bool unit_work(uint32_t tS, uint32_t cl, uint8_t *dst, int row, bool row_ok, Bars *bars,
-                                          int g, int x, uint32_t use, uint32_t nx, const Params &p,
+// A unit for one lane (one key), 32 queries at a time (rolled: the two groups
+// walk this code at different places, and the longer straight line missed the
+// instruction cache): P to TMEM over D, dS to the lane's row of the
+// shared-memory chunk (128-byte swizzle).  halves: 32-query parts inside the
+// block.  cl: the queries' -lse log2e, and 256 floats on their -delta.  Keys
+// past the block (not row_ok) give dS = 0: dQ sums over all keys of the MMAs'
+// 16-row granule.
+__device__ __forceinline__ bool unit_work(uint32_t tS, uint32_t cl, uint8_t *dst, int row, bool row_ok, int halves,
+                                          Bars *bars, int g, int x, uint32_t use, uint32_t nx, const Params &p,
                                           volatile int *abort_flag)
 {
     if (!wait_bar(smem_u32(&bars->s_full[g]), use & 1, abort_flag, p.wait_ns, p.status))
         return false;
     tc_fence_after();
-    uint32_t s[32 * NH];
-#pragma unroll
-    for (int h = 0; h < NH; ++h)
-        tmem_ld32_nowait(tS + 32 * h, s + 32 * h);
-    tmem_wait_ld();
-#pragma unroll
-    for (int i = 0; i < 32 * NH; ++i)
-        reg_fence(s[i]);
-    tc_fence_before();
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0)
-        mbar_arrive(smem_u32(&bars->s_empty[g]));
     const uint64_t k2 = pair(p.scale_log2, p.scale_log2);
-    uint64_t pr[16 * NH];
+    const uint32_t tP = tS + kDCol;
+#pragma unroll 1
+    for (int h = 0; h < halves; ++h) {
+        uint32_t s[32];
+        tmem_ld32_nowait(tS + 32 * h, s);
+        tmem_wait_ld();
 #pragma unroll
-    for (int q = 0; q < 8 * NH; ++q) {
-        uint64_t l0, l1;
-        lds_pairs(cl + 16 * q, l0, l1);
-        const uint64_t y0 = fma2(pair(s[4 * q], s[4 * q + 1]), k2, l0);
-        const uint64_t y1 = fma2(pair(s[4 * q + 2], s[4 * q + 3]), k2, l1);
-        float a, b;
-        unpair(y0, a, b);
-        pr[2 * q] = pair(ex2_approx(a), ex2_approx(b));
-        unpair(y1, a, b);
-        pr[2 * q + 1] = pair(ex2_approx(a), ex2_approx(b));
-        if (q & 1) {   // at most two loads ahead of their use (registers)
-            pair_fence(pr[2 * q]);
-            pair_fence(pr[2 * q + 1]);
+        for (int i = 0; i < 32; ++i)
+            reg_fence(s[i]);
+        if (h + 1 == halves) {
+            tc_fence_before();
+            __syncwarp();
+            if ((threadIdx.x & 31) == 0)
+                mbar_arrive(smem_u32(&bars->s_empty[g]));
         }
-    }
-    if (!wait_bar(smem_u32(&bars->d_full[g]), use & 1, abort_flag, p.wait_ns, p.status))
-        return false;
-    // the last key tile's dQ no longer reads this half's chunks
-    if (nx > 0 && !wait_bar(smem_u32(&bars->dq_done[x]), (nx - 1) & 1, abort_flag, p.wait_ns, p.status))
-        return false;
-    tc_fence_after();
+        uint64_t pr[16];
 #pragma unroll
-    for (int h = 0; h < NH; ++h) {
-        uint32_t d[32];
-        tmem_ld32_nowait(tS + kDCol + 32 * h, d);
+        for (int q = 0; q < 8; ++q) {
+            uint64_t l0, l1;
+            lds_pairs(cl + 128 * h + 16 * q, l0, l1);
+            const uint64_t y0 = fma2(pair(s[4 * q], s[4 * q + 1]), k2, l0);
+            const uint64_t y1 = fma2(pair(s[4 * q + 2], s[4 * q + 3]), k2, l1);
+            float a, b;
+            unpair(y0, a, b);
+            pr[2 * q] = pair(ex2_approx(a), ex2_approx(b));
+            unpair(y1, a, b);
+            pr[2 * q + 1] = pair(ex2_approx(a), ex2_approx(b));
+        }
+        // D, and the last key tile's dQ no longer reads this half's chunks
+        if (h == 0 && (!wait_bar(smem_u32(&bars->d_full[g]), use & 1, abort_flag, p.wait_ns, p.status) ||
+                       (nx > 0 &&
+                        !wait_bar(smem_u32(&bars->dq_done[x]), (nx - 1) & 1, abort_flag, p.wait_ns, p.status))))
+            return false;
+        tc_fence_after();
+        uint32_t d[32], pk[16];
+        tmem_ld32_nowait(tP + 32 * h, d);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float a, b;
+            unpair(pr[i], a, b);
+            pk[i] = pack_bf16x2(a, b);
+        }
         tmem_wait_ld();
 #pragma unroll
         for (int i = 0; i < 32; ++i)
             reg_fence(d[i]);
-        if (h == 0) {   // P over the half of D that is in registers
-#pragma unroll
-            for (int k = 0; k < NH; ++k) {
-                uint32_t pk[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    float a, b;
-                    unpair(pr[16 * k + i], a, b);
-                    pk[i] = pack_bf16x2(a, b);
-                }
-                tmem_st16p(tS + kDCol + 16 * k, pk);
-            }
-        }
+        tmem_st16p(tP + 16 * h, pk);   // over columns of D that are in registers or past
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            uint32_t pk[4];
+            uint32_t o[4];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const int q = 2 * i + j, r = 8 * h + q;
+                const int q = 2 * i + j;
                 uint64_t l0, l1;
-                lds_pairs(cl + 1024 + 16 * r, l0, l1);
-                uint64_t g0 = mul2(pr[2 * r], add2(pair(d[4 * q], d[4 * q + 1]), l0));
-                uint64_t g1 = mul2(pr[2 * r + 1], add2(pair(d[4 * q + 2], d[4 * q + 3]), l1));
-                pair_fence(g0);
-                pair_fence(g1);
+                lds_pairs(cl + 1024 + 128 * h + 16 * q, l0, l1);
+                const uint64_t g0 = mul2(pr[2 * q], add2(pair(d[4 * q], d[4 * q + 1]), l0));
+                const uint64_t g1 = mul2(pr[2 * q + 1], add2(pair(d[4 * q + 2], d[4 * q + 3]), l1));
                 float a, b;
                 unpair(g0, a, b);
-                pk[2 * j] = row_ok ? pack_bf16x2(a, b) : 0u;
+                o[2 * j] = row_ok ? pack_bf16x2(a, b) : 0u;
                 unpair(g1, a, b);
-                pk[2 * j + 1] = row_ok ? pack_bf16x2(a, b) : 0u;
+                o[2 * j + 1] = row_ok ? pack_bf16x2(a, b) : 0u;
             }
-            *reinterpret_cast<uint4 *>(dst + ((4 * h + i) ^ (row & 7)) * 16) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            *reinterpret_cast<uint4 *>(dst + ((4 * h + i) ^ (row & 7)) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
         }
     }
     fence_proxy_async_smem();
@@ -266,7 +259,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&bars->m_empty[s]), 1);
         }
         for (int g = 0; g < 2; ++g) {
-            mbar_init(smem_u32(&bars->ready[g]), 1);
+            mbar_init(smem_u32(&bars->ready_s[g]), 1);
+            mbar_init(smem_u32(&bars->ready_d[g]), 1);
             mbar_init(smem_u32(&bars->cols_empty[g]), kElemWarps);
             mbar_init(smem_u32(&bars->s_full[g]), 1);
             mbar_init(smem_u32(&bars->d_full[g]), 1);
@@ -276,6 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&bars->dq_done[g]), 1);
             mbar_init(smem_u32(&bars->mma_done[g]), 1);
         }
+        mbar_init(smem_u32(&bars->idle), kElemWarps / 2);
         mbar_init(smem_u32(&bars->acc_full), 1);
         mbar_init(smem_u32(&bars->acc_empty), 4);
         mbar_init(smem_u32(&bars->dq_empty), 4);
@@ -307,7 +302,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     if (warp < kEpi0) {
-        few_regs();
         if (warp == 0) {
             // ======================================================== producer
             PlanWalker w;
@@ -316,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t pol = policy_evict_first();   // every matrix is read once
             const uint32_t bytes = (uint32_t)p.block * kRowBytes;
             int n = 0;      // items published
-            int nm = 0;     // matrices claimed
+            int last = kMats;   // matrices claimed of the last of them
             bool stop = false;
             auto publish = [&](const ItemDesc &d) -> bool {
                 const int j = n % kDescRing;
@@ -341,54 +335,60 @@ __global__ void __launch_bounds__(kThreads, 1)
                     stop = true;
                     break;
                 }
-                for (int m = 0; m < kMats; ++m) {
-                    const int s = nm % p.slots, u = nm / p.slots;
-                    if (u > 0 && !wait(&bars->m_empty[s], (uint32_t)(u - 1))) {
+                // V's slot is free after the last item's last D, dO's after its
+                // last dV: both before the item's end
+                for (last = 0; last < kMats; ++last) {
+                    const int m = last < 2 ? last : last == 2 ? kMatV : kMatO;
+                    const Slot s(m, n - 1, p.slots);
+                    if (s.use > 0 && !wait(&bars->m_empty[s.at], (uint32_t)(s.use - 1))) {
                         stop = true;
                         break;
                     }
-                    if (lane == 0 && !(skip0 && nm == 0)) {
-                        const uint32_t bar = smem_u32(&bars->m_full[s]);
+                    if (lane == 0 && !(skip0 && n == 1 && last == 0)) {
+                        const uint32_t bar = smem_u32(&bars->m_full[s.at]);
                         mbar_arrive_expect_tx(bar, bytes);
-                        tma_load_2d(base + s * p.slot_bytes, m == 0 ? &tm_k : m == 1 ? &tm_q : m == 2 ? &tm_v : &tm_do,
-                                    d.h * 64, d.f0, bar, pol);
+                        tma_load_2d(base + s.at * p.slot_bytes,
+                                    m == kMatK ? &tm_k : m == kMatQ ? &tm_q : m == kMatV ? &tm_v : &tm_do, d.h * 64,
+                                    d.f0, bar, pol);
                     }
                     __syncwarp();
-                    ++nm;
                 }
             }
             if (w.bad && lane == 0)
                 report(p.status, NLE_ERR_INVALID_ARG);
+            const int items = n;
             if (!stop)
                 publish(ItemDesc{0, -1, 0});
             // drain: the last copy into each slot must land before exit
             if (lane == 0)
-                for (int m = nm - p.slots; m < nm; ++m)
-                    if (m >= 0 && !(skip0 && m == 0))
-                        wait_bar_drain(smem_u32(&bars->m_full[m % p.slots]), (uint32_t)(m / p.slots) & 1, wait_ns);
+                for (int j = 0; j < kMats; ++j) {
+                    const int m = j < 2 ? j : j == 2 ? kMatV : kMatO;
+                    const int claimed = items - (j >= last ? 1 : 0);
+                    for (int i = max(claimed - (m < p.slots - kMats ? 2 : 1), 0); i < claimed; ++i) {
+                        const Slot s(m, i, p.slots);
+                        if (!(skip0 && i == 0 && j == 0))
+                            wait_bar_drain(smem_u32(&bars->m_full[s.at]), (uint32_t)s.use & 1, wait_ns);
+                    }
+                }
             __syncwarp();
         } else if (warp == 1) {
             // ======================================================== S and D MMAs
             DescReader rd{0};
             ItemDesc d;
             uint32_t n = 0, t = 0;   // items, units
-            int slot = 0;
             bool ok = true;
             while (ok && rd.next(bars, p, abort_flag, d)) {
-                if (!wait(&bars->ready[n & 1], n >> 1))
+                if (!wait(&bars->ready_s[n & 1], n >> 1))
                     break;
                 const int L = __shfl_sync(kFull, d.L, 0);
-                uint32_t at[kMats];
-    #pragma unroll
-                for (int m = 0; m < kMats; ++m) {
-                    at[m] = base + slot * p.slot_bytes;
-                    slot = slot + 1 == p.slots ? 0 : slot + 1;
-                }
-                const uint64_t dk0 = smem_desc_sw128(at[0], 16, 1024), dq0 = smem_desc_sw128(at[1], 16, 1024);
-                const uint64_t dv0 = smem_desc_sw128(at[2], 16, 1024), do0 = smem_desc_sw128(at[3], 16, 1024);
+                auto mat = [&](int m) {
+                    return smem_desc_sw128(base + Slot(m, (int)n, p.slots).at * p.slot_bytes, 16, 1024);
+                };
+                const uint64_t dk0 = mat(kMatK), dq0 = mat(kMatQ), dv0 = mat(kMatV), do0 = mat(kMatO);
+                const int v_slot = Slot(kMatV, (int)n, p.slots).at;
                 const int nu = (L + kUnit - 1) / kUnit, units = nu * ((L + kKeys - 1) / kKeys);
-                // S runs one unit ahead of D (inside the item: the next item's
-                // matrices may wait for this one's end)
+                // S runs one unit ahead of D, the item's first before its V and
+                // dO have arrived
                 int sc = 0, su = 0, dc = 0, du = 0;   // key tile and 64-query part of the next S and D
                 for (int i = 0; ok && i <= units; ++i) {
                     if (i < units) {
@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc_fence_after();
                         // K steps of 16 elements = 32 bytes inside the 128-byte swizzle atom
                         if (elect_one()) {
-    #pragma unroll
+#pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
                                 mma_ss(tmem + g * kGroupCols, a + 2 * kk, b + 2 * kk, id, kk > 0 ? 1u : 0u);
                             mma_commit(smem_u32(&bars->s_full[g]));
@@ -417,16 +417,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint32_t g = (t + i - 1) & 1, use = (t + i - 1) >> 1;
                         const uint32_t id = idesc_bf16_f32(128, min(kUnit, (L - du * kUnit + 15) & ~15), false);
                         const uint64_t a = dv0 + dc * (kTileBytes >> 4), b = do0 + du * (kUnit * kRowBytes >> 4);
-                        if (use > 0 && !wait(&bars->p_empty[g], use - 1)) {
+                        if ((i == 1 && !wait(&bars->ready_d[n & 1], n >> 1)) ||
+                            (use > 0 && !wait(&bars->p_empty[g], use - 1))) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
                         if (elect_one()) {
-    #pragma unroll
+#pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
                                 mma_ss(tmem + g * kGroupCols + kDCol, a + 2 * kk, b + 2 * kk, id, kk > 0 ? 1u : 0u);
                             mma_commit(smem_u32(&bars->d_full[g]));
+                            if (i == units)
+                                mma_commit(smem_u32(&bars->m_empty[v_slot]));
                         }
                         __syncwarp();
                         if (++du == nu) {
@@ -448,23 +451,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ======================================================== dV, dK and dQ MMAs
             DescReader rd{0};
             ItemDesc d;
-            uint32_t t = 0, kt = 0, n = 0;   // units, key tiles, items
-            int slot = 0;
+            uint32_t t = 0, kt = 0, n = 0, idle = 0;   // units, key tiles, items, items of one unit
             constexpr uint32_t id = idesc_bf16_f32(128, 64, true), id_q = id | (1u << 15);   // id_q: A is M-major too
             bool ok = true;
             while (ok && rd.next(bars, p, abort_flag, d)) {
                 const int L = __shfl_sync(kFull, d.L, 0);
-                uint32_t at[kMats];
-                const int slot0 = slot;
-    #pragma unroll
-                for (int m = 0; m < kMats; ++m) {
-                    at[m] = base + slot * p.slot_bytes;
-                    slot = slot + 1 == p.slots ? 0 : slot + 1;
-                }
+                const int sk = Slot(kMatK, (int)n, p.slots).at, sq = Slot(kMatQ, (int)n, p.slots).at;
+                const int so = Slot(kMatO, (int)n, p.slots).at;
                 // N = 64 is one 128-byte swizzle atom along N; K steps of 16 rows
                 // advance the start by 2048 bytes
-                const uint64_t bk = smem_desc_sw128(at[0], 0, 1024), bq = smem_desc_sw128(at[1], 0, 1024);
-                const uint64_t bo = smem_desc_sw128(at[3], 0, 1024);
+                const uint64_t bk = smem_desc_sw128(base + sk * p.slot_bytes, 0, 1024);
+                const uint64_t bq = smem_desc_sw128(base + sq * p.slot_bytes, 0, 1024);
+                const uint64_t bo = smem_desc_sw128(base + so * p.slot_bytes, 0, 1024);
                 for (int c = 0; ok && c * kKeys < L; ++c, ++kt) {
                     // the last tile's dK and dV have been read
                     if (kt > 0 && !wait(&bars->acc_empty, kt - 1)) {
@@ -475,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const bool last_c = (c + 1) * kKeys >= L;
                     for (int u = 0; u * kUnit < L; ++u, ++t) {
                         const uint32_t g = t & 1;
-                        if (!wait(&bars->p_full[g], t >> 1)) {
+                        if (!wait(&bars->p_full[g], t >> 1) || (L <= kUnit && !wait(&bars->idle, idle++))) {
                             ok = false;
                             break;
                         }
@@ -491,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             break;
                         }
                         if (elect_one()) {
-    #pragma unroll
+#pragma unroll
                             for (int kk = 0; kk < 4; ++kk) {
                                 if (kk < steps) {
                                     const uint64_t row = ub + kk * (16 * kRowBytes >> 4);
@@ -501,6 +499,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 }
                             }
                             mma_commit(smem_u32(&bars->p_empty[g]));
+                            if (last_u && last_c) {   // dO and Q are free
+                                mma_commit(smem_u32(&bars->m_empty[so]));
+                                mma_commit(smem_u32(&bars->m_empty[sq]));
+                            }
                             if ((u & 1) || last_u) {
                                 const int x = u >> 1;
                                 const uint64_t aq = smem_desc_sw128(ds_base + 2 * x * kChunkBytes, kChunkBytes, 1024);
@@ -513,10 +515,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                             if (last_u) {
                                 mma_commit(smem_u32(&bars->acc_full));
-                                if (last_c)   // the item's matrices are free
-                                    for (int m = 0; m < kMats; ++m)
-                                        mma_commit(smem_u32(&bars->m_empty[slot0 + m < p.slots ? slot0 + m
-                                                                                               : slot0 + m - p.slots]));
+                                if (last_c)
+                                    mma_commit(smem_u32(&bars->m_empty[sk]));
                             }
                         }
                         __syncwarp();
@@ -534,12 +534,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             DescReader rd{0};
             ItemDesc d;
             uint32_t n = 0;
-            int nm = 0;
             bool ok = true;
             while (ok && rd.next(bars, p, abort_flag, d)) {
                 float l[8], dl[8];
                 const size_t at = (size_t)d.h * p.total + d.f0;
-    #pragma unroll
+#pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int c = lane + 32 * i;
                     l[i] = c < d.L ? __ldg(p.lse + at + c) : INFINITY;
@@ -548,35 +547,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (n >= 2 && !wait(&bars->cols_empty[n & 1], (n >> 1) - 1))
                     break;
                 float *cl = cols + (n & 1) * 512;
-    #pragma unroll
+#pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     cl[lane + 32 * i] = l[i] * -kLog2e;
                     cl[256 + lane + 32 * i] = -dl[i];
                 }
                 const int pad = -d.L & 15;
-                for (int m = 0; m < kMats; ++m, ++nm) {
-                    const int s = nm % p.slots;
-                    if (!wait(&bars->m_full[s], (uint32_t)(nm / p.slots))) {
-                        ok = false;
-                        break;
+                for (int half = 0; ok && half < 2; ++half) {   // K and Q, then V and dO
+                    for (int m = 2 * half; m < 2 * half + 2; ++m) {
+                        const Slot s(m, (int)n, p.slots);
+                        if (!wait(&bars->m_full[s.at], (uint32_t)s.use)) {
+                            ok = false;
+                            break;
+                        }
+                        uint4 *z = reinterpret_cast<uint4 *>(smem + s.at * p.slot_bytes + d.L * kRowBytes);
+                        for (int i = lane; i < pad * (kRowBytes / 16); i += 32)
+                            z[i] = make_uint4(0, 0, 0, 0);
                     }
-                    uint4 *z = reinterpret_cast<uint4 *>(smem + s * p.slot_bytes + d.L * kRowBytes);
-                    for (int i = lane; i < pad * (kRowBytes / 16); i += 32)
-                        z[i] = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (ok && lane == 0)
+                        mbar_arrive(smem_u32(&(half ? bars->ready_d : bars->ready_s)[n & 1]));
+                    __syncwarp();
                 }
-                if (!ok)
-                    break;
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(smem_u32(&bars->ready[n & 1]));
-                __syncwarp();
                 ++n;
             }
         }
     } else if (warp < kElem0) {
         // ======================================================== results
-        few_regs();
         const int qq = warp & 3;   // TMEM lane quarter of this warp
         const uint32_t lanes = (uint32_t)(qq * 32) << 16;
         DescReader rd{0};
@@ -632,7 +630,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         // ======================================================== elementwise
-        more_regs();
         const int g = (warp - kElem0) >> 2;          // group
         const int qq = warp & 3;                     // TMEM lane quarter of this warp
         const int row = qq * 32 + lane;              // key of the tile
@@ -644,24 +641,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t nx0 = 0, nx1 = 0;           // key tiles that had queries in half 0, 1 of the block
         bool ok = true;
         for (; ok && rd.next(bars, p, abort_flag, d); ++n) {
-            if (!wait(&bars->ready[n & 1], n >> 1))
+            if (!wait(&bars->ready_s[n & 1], n >> 1))
                 break;
             const uint32_t cl = smem_u32(cols) + (n & 1) * 2048;
             for (int c = 0; ok && c * kKeys < d.L; ++c) {
                 const bool active = c * kKeys + qq * 32 < d.L;   // warp-uniform
                 const bool row_ok = c * kKeys + row < d.L;
                 // the group's units of the tile
-                for (int u = (t ^ g) & 1; u * kUnit < d.L; u += 2) {
+                const int u0 = (t ^ g) & 1;
+                for (int u = u0; u * kUnit < d.L; u += 2) {
                     const uint32_t use = (t + u) >> 1;
                     const int c0 = u * kUnit;           // first query of the unit
                     const bool two = c0 + 32 < d.L;    // warp-uniform: queries in the unit's second half
                     const uint32_t nx = u >> 1 ? nx1 : nx0;
                     uint8_t *dst = smem + p.ds_off + u * kChunkBytes + row * kRowBytes;
-                    const uint32_t uc = cl + 4 * c0;
                     const int x = u >> 1;
                     ok = !active ? unit_idle(bars, g, x, use, nx, p, abort_flag)
-                         : two   ? unit_work<2>(tS, uc, dst, row, row_ok, bars, g, x, use, nx, p, abort_flag)
-                                 : unit_work<1>(tS, uc, dst, row, row_ok, bars, g, x, use, nx, p, abort_flag);
+                                 : unit_work(tS, cl + 4 * c0, dst, row, row_ok, two ? 2 : 1, bars, g, x, use, nx, p,
+                                             abort_flag);
+                    // no unit of this group in the other half: its phase is
+                    // waited for all the same, before the half's next one can
+                    // end (a parity wait only tells the phase before apart)
+                    if (ok && d.L > kKeys && (2 + u0) * kUnit >= d.L && nx1 > 0 && !wait(&bars->dq_done[1], nx1 - 1))
+                        ok = false;
                     if (!ok)
                         break;
                     tc_fence_before();
@@ -669,12 +671,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0)
                         mbar_arrive(smem_u32(&bars->p_full[g]));
                 }
-                // a half without a unit for this group: its phase is waited for
-                // all the same (a parity wait only tells the phase before apart)
-                const int u0 = (t ^ g) & 1;
-                if (ok && ((u0 * kUnit >= d.L && nx0 > 0 && !wait(&bars->dq_done[0], nx0 - 1)) ||
-                           (d.L > kKeys && (2 + u0) * kUnit >= d.L && nx1 > 0 && !wait(&bars->dq_done[1], nx1 - 1))))
-                    ok = false;
+                if (ok && u0 * kUnit >= d.L) {   // no unit at all: the same, and warp 2 waits for it
+                    if (nx0 > 0 && !wait(&bars->dq_done[0], nx0 - 1))
+                        ok = false;
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(smem_u32(&bars->idle));
+                }
                 t += (d.L + kUnit - 1) / kUnit;
                 ++nx0;
                 nx1 += d.L > kKeys;
