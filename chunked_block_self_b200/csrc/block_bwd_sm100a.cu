@@ -81,8 +81,9 @@ struct Bars {
     uint64_t cols_empty[2];         // kElemWarps arrivals: the item's columns are no longer read
     uint64_t s_full[2], d_full[2];  // by group
     uint64_t s_empty[2];            // 4 arrivals: S has been read
-    uint64_t p_full[2];             // 4 arrivals: P and dS written
-    uint64_t p_empty[2];            // the unit's dV and dK MMAs have completed (P, over D)
+    uint64_t p_full[2];             // 4 arrivals: P written, D read
+    uint64_t ds_full[4];            // by unit & 3; 4 arrivals: dS written
+    uint64_t p_empty[2];            // the unit's dV MMAs have completed (P, over D)
     uint64_t dq_done[2];            // the key tile's dQ_x MMAs have completed (dS chunks 2x, 2x + 1)
     uint64_t idle;                  // 4 arrivals: the group without a unit in an item of one unit
     uint64_t acc_full;              // the key tile's sums (the item's, on its last) are complete
@@ -109,6 +110,14 @@ struct Params {
     unsigned long long wait_ns;
     int flags;
 };
+
+// A box into L2, ahead of its load.
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap *tm, int x, int y)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];"
+                 ::"l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y)
+                 : "memory");
+}
 
 // Matrix m of item n: the first slots - 4 of K, Q, dO, V have two slots each.
 struct Slot {
@@ -149,6 +158,9 @@ __device__ __forceinline__ bool unit_idle(Bars *bars, int g, int x, uint32_t use
         mbar_arrive(smem_u32(&bars->s_empty[g]));
     if (!wait_bar(smem_u32(&bars->d_full[g]), use & 1, abort_flag, p.wait_ns, p.status))
         return false;
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0)
+        mbar_arrive(smem_u32(&bars->p_full[g]));
     return nx == 0 || wait_bar(smem_u32(&bars->dq_done[x]), (nx - 1) & 1, abort_flag, p.wait_ns, p.status);
 }
 
@@ -214,6 +226,13 @@ __device__ __forceinline__ bool unit_work(uint32_t tS, uint32_t cl, uint8_t *dst
         for (int i = 0; i < 32; ++i)
             reg_fence(d[i]);
         tmem_st16p(tP + 16 * h, pk);   // over columns of D that are in registers or past
+        if (h + 1 == halves) {   // dV, and after it the next unit's D, need not wait for dS
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if ((threadIdx.x & 31) == 0)
+                mbar_arrive(smem_u32(&bars->p_full[g]));
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             uint32_t o[4];
@@ -234,7 +253,6 @@ __device__ __forceinline__ bool unit_work(uint32_t tS, uint32_t cl, uint8_t *dst
         }
     }
     fence_proxy_async_smem();
-    tmem_wait_st();
     return true;
 }
 
@@ -266,6 +284,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&bars->d_full[g]), 1);
             mbar_init(smem_u32(&bars->s_empty[g]), kElemWarps / 2);
             mbar_init(smem_u32(&bars->p_full[g]), kElemWarps / 2);
+            mbar_init(smem_u32(&bars->ds_full[g]), kElemWarps / 2);
+            mbar_init(smem_u32(&bars->ds_full[2 + g]), kElemWarps / 2);
             mbar_init(smem_u32(&bars->p_empty[g]), 1);
             mbar_init(smem_u32(&bars->dq_done[g]), 1);
             mbar_init(smem_u32(&bars->mma_done[g]), 1);
@@ -339,6 +359,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // last dV: both before the item's end
                 for (last = 0; last < kMats; ++last) {
                     const int m = last < 2 ? last : last == 2 ? kMatV : kMatO;
+                    if (last == 2 && n > 1 && lane == 0) {
+                        tma_prefetch_2d(&tm_v, d.h * 64, d.f0);
+                        tma_prefetch_2d(&tm_do, d.h * 64, d.f0);
+                    }
                     const Slot s(m, n - 1, p.slots);
                     if (s.use > 0 && !wait(&bars->m_empty[s.at], (uint32_t)(s.use - 1))) {
                         stop = true;
@@ -387,12 +411,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint64_t dk0 = mat(kMatK), dq0 = mat(kMatQ), dv0 = mat(kMatV), do0 = mat(kMatO);
                 const int v_slot = Slot(kMatV, (int)n, p.slots).at;
                 const int nu = (L + kUnit - 1) / kUnit, units = nu * ((L + kKeys - 1) / kKeys);
-                // S runs one unit ahead of D, the item's first before its V and
-                // dO have arrived
+                // the item's first two S before its V and dO have arrived; then
+                // S and D of a unit in turn, as the units before them end
                 int sc = 0, su = 0, dc = 0, du = 0;   // key tile and 64-query part of the next S and D
-                for (int i = 0; ok && i <= units; ++i) {
-                    if (i < units) {
-                        const uint32_t g = (t + i) & 1, use = (t + i) >> 1;
+                for (int i = 0, si = 0; ok && i < units; ++i) {
+                    for (; ok && si < units && si < max(i + 1, 2); ++si) {
+                        const uint32_t g = (t + si) & 1, use = (t + si) >> 1;
                         const uint32_t id = idesc_bf16_f32(128, min(kUnit, (L - su * kUnit + 15) & ~15), false);
                         const uint64_t a = dk0 + sc * (kTileBytes >> 4), b = dq0 + su * (kUnit * kRowBytes >> 4);
                         if (use > 0 && !wait(&bars->s_empty[g], use - 1)) {
@@ -413,29 +437,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                             ++sc;
                         }
                     }
-                    if (i > 0) {
-                        const uint32_t g = (t + i - 1) & 1, use = (t + i - 1) >> 1;
-                        const uint32_t id = idesc_bf16_f32(128, min(kUnit, (L - du * kUnit + 15) & ~15), false);
-                        const uint64_t a = dv0 + dc * (kTileBytes >> 4), b = do0 + du * (kUnit * kRowBytes >> 4);
-                        if ((i == 1 && !wait(&bars->ready_d[n & 1], n >> 1)) ||
-                            (use > 0 && !wait(&bars->p_empty[g], use - 1))) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        if (elect_one()) {
+                    const uint32_t g = (t + i) & 1, use = (t + i) >> 1;
+                    const uint32_t id = idesc_bf16_f32(128, min(kUnit, (L - du * kUnit + 15) & ~15), false);
+                    const uint64_t a = dv0 + dc * (kTileBytes >> 4), b = do0 + du * (kUnit * kRowBytes >> 4);
+                    if (!ok || (i == 0 && !wait(&bars->ready_d[n & 1], n >> 1)) ||
+                        (use > 0 && !wait(&bars->p_empty[g], use - 1))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    if (elect_one()) {
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                mma_ss(tmem + g * kGroupCols + kDCol, a + 2 * kk, b + 2 * kk, id, kk > 0 ? 1u : 0u);
-                            mma_commit(smem_u32(&bars->d_full[g]));
-                            if (i == units)
-                                mma_commit(smem_u32(&bars->m_empty[v_slot]));
-                        }
-                        __syncwarp();
-                        if (++du == nu) {
-                            du = 0;
-                            ++dc;
-                        }
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_ss(tmem + g * kGroupCols + kDCol, a + 2 * kk, b + 2 * kk, id, kk > 0 ? 1u : 0u);
+                        mma_commit(smem_u32(&bars->d_full[g]));
+                        if (i + 1 == units)
+                            mma_commit(smem_u32(&bars->m_empty[v_slot]));
+                    }
+                    __syncwarp();
+                    if (++du == nu) {
+                        du = 0;
+                        ++dc;
                     }
                 }
                 t += units;
@@ -473,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const bool last_c = (c + 1) * kKeys >= L;
                     for (int u = 0; u * kUnit < L; ++u, ++t) {
                         const uint32_t g = t & 1;
-                        if (!wait(&bars->p_full[g], t >> 1) || (L <= kUnit && !wait(&bars->idle, idle++))) {
+                        if (!wait(&bars->p_full[g], t >> 1)) {
                             ok = false;
                             break;
                         }
@@ -483,26 +505,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint64_t ak = smem_desc_sw128(ds_base + u * kChunkBytes, 16, 1024);
                         const bool last_u = (u + 1) * kUnit >= L;
                         const uint32_t ap = tmem + g * kGroupCols + kDCol;
-                        // the item's first dQ: the last item's has been read
-                        if (c == 0 && (u == 1 || (u == 0 && last_u)) && n > 0 && !wait(&bars->dq_empty, n - 1)) {
+                        if (elect_one()) {
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                if (kk < steps)
+                                    mma_ts(tmem + kVAcc, ap + kk * 8, bo + ub + kk * (16 * kRowBytes >> 4), id,
+                                           u > 0 || kk > 0 ? 1u : 0u);
+                            mma_commit(smem_u32(&bars->p_empty[g]));
+                            if (last_u && last_c)
+                                mma_commit(smem_u32(&bars->m_empty[so]));
+                        }
+                        __syncwarp();
+                        // dS; and for the item's first dQ: the last item's has been read
+                        if (!wait(&bars->ds_full[t & 3], t >> 2) || (L <= kUnit && !wait(&bars->idle, idle++)) ||
+                            (c == 0 && (u == 1 || (u == 0 && last_u)) && n > 0 && !wait(&bars->dq_empty, n - 1))) {
                             ok = false;
                             break;
                         }
                         if (elect_one()) {
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk) {
-                                if (kk < steps) {
-                                    const uint64_t row = ub + kk * (16 * kRowBytes >> 4);
-                                    const uint32_t acc = u > 0 || kk > 0 ? 1u : 0u;
-                                    mma_ts(tmem + kVAcc, ap + kk * 8, bo + row, id, acc);
-                                    mma_ss(tmem + kKAcc, ak + 2 * kk, bq + row, id, acc);
-                                }
-                            }
-                            mma_commit(smem_u32(&bars->p_empty[g]));
-                            if (last_u && last_c) {   // dO and Q are free
-                                mma_commit(smem_u32(&bars->m_empty[so]));
+                            for (int kk = 0; kk < 4; ++kk)
+                                if (kk < steps)
+                                    mma_ss(tmem + kKAcc, ak + 2 * kk, bq + ub + kk * (16 * kRowBytes >> 4), id,
+                                           u > 0 || kk > 0 ? 1u : 0u);
+                            if (last_u && last_c)
                                 mma_commit(smem_u32(&bars->m_empty[sq]));
-                            }
                             if ((u & 1) || last_u) {
                                 const int x = u >> 1;
                                 const uint64_t aq = smem_desc_sw128(ds_base + 2 * x * kChunkBytes, kChunkBytes, 1024);
@@ -666,10 +693,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ok = false;
                     if (!ok)
                         break;
-                    tc_fence_before();
                     __syncwarp();
                     if (lane == 0)
-                        mbar_arrive(smem_u32(&bars->p_full[g]));
+                        mbar_arrive(smem_u32(&bars->ds_full[(t + u) & 3]));
                 }
                 if (ok && u0 * kUnit >= d.L) {   // no unit at all: the same, and warp 2 waits for it
                     if (nx0 > 0 && !wait(&bars->dq_done[0], nx0 - 1))
