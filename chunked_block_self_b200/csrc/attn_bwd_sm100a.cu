@@ -768,10 +768,10 @@ int launch_attn_bwd(const nle_attn_bwd_args *a, int block, void *stream)
     if (cudaGetLastError() != cudaSuccess)
         return NLE_ERR_CUDA;
     // Blocks of more than one key tile, and at least one (block, head) per SM:
-    // whole blocks on chip (batch-128 workload: 443 us against 490 us here, with
-    // delta's 41 us in both).  One key tile leaves that kernel's second half
-    // idle (128-frame blocks: 411 against 343 us), and fewer items leave SMs
-    // idle (64 items: 17.0 against 13.7 us; 160: 19.2 against 20.9 us).
+    // whole blocks on chip (batch of 128 utterances: 395 us against 491 us here,
+    // with delta's 41 us in both).  One key tile leaves that kernel's second half
+    // idle (128-frame blocks: 372 against 344 us), and fewer items leave SMs
+    // idle (64 items: 17.1 against 14.0 us; 128: 19.0 against 21.0 us).
     const bool whole = block && !(a->flags & NLE_FLAG_SPLIT_ITEMS) &&
                        ((a->flags & NLE_FLAG_WHOLE_ITEMS) || (block > kRows && units * a->heads >= di.sm_count));
     if (whole) {

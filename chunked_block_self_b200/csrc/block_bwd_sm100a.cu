@@ -17,27 +17,36 @@
 // 128-byte swizzled: a row-major operand for dK and a column-major one for dQ.
 //
 // One persistent CTA per SM, 16 warps:
-//   warp 0   TMA producer: K, Q, V, dO of an item, one box each, into a ring
-//            of matrix slots; publishes the item's descriptor.
-//   warp 1   issues S (one unit ahead) and D.
-//   warp 2   issues dV, dK and dQ.
+//   warp 0   TMA producer: K, Q, V, dO of an item, one box each; publishes the
+//            item's descriptor.  Where dS leaves room for more than one item's
+//            matrices, K, Q, dO, V have two slots each in that order; of the
+//            others the next item's are fetched into L2 meanwhile.
+//   warp 1   issues S and D: an item's first two S before its V and dO are
+//            there, then S and D of a unit in turn.
+//   warp 2   issues dV (as soon as P is written), dK and dQ.
 //   warp 3   owns TMEM; zeroes operand rows past the block (up to the MMAs'
 //            16-row granule: their P and dS are 0, but 0 * Inf would be NaN)
 //            and stages the block's lse and delta (+inf and 0 past it).
 //   warps 4-7   results: a key tile's dK and dV, an item's dQ.
 //   warps 8-15  elementwise, two groups of four warps on alternate units
 //            (group g: S, D buffer g): a lane owns one key of the tile.
-// Registers are what this division is for: beside 200 KB of shared memory a
-// spill lives in L2, and 120 bytes of them a thread cost 40 % of the time.
-//
-// What bounds it: six 25 KB slots fit beside dS, so V and dO of the next
-// 200-frame block are loaded only when this one's products are done, about
-// 7 k of the 23 k cycles that an item takes; its eight units' chain (S, exp, D,
-// dS, accumulate) takes the rest, the exps 4 k, the products 5 k of it.  The
-// batch of 128 utterances (16 heads, blocks of 200): 0.40 ms without delta.
 // TMEM (512 columns): S, D of group g at 128 g and 128 g + 64 (P over D's
 // first 32 columns, so that the group's next S need not wait for dV), dQ_0,
 // dQ_1 at 256 and 320, dK at 384, dV at 448.
+//
+// What bounds it: a 200-frame block of one head takes 17 k cycles.  2.7 k of
+// them wait for its V and dO, which have one slot each; its eight units follow
+// at 1.8 k each, two in flight: the elementwise work of one is about 2 k (512
+// for its exps), the hops between its warps and the issue of its MMAs as much
+// again, the tensor pipe busy for 0.9 k.  HBM would allow 8 k.  The batch of
+// 128 utterances (16 heads, 58,903 frames, 5,648 blocks): 0.36 ms, and 0.04 ms
+// for delta: 2.4 TB/s of the operator's bytes.  Steps that paid: three
+// warpgroups' registers without spills (388 -> 293 us on a batch of 34,512
+// frames; beside 200 KB of shared memory a spill lives in L2), results on warps
+// of their own and S ahead (-> 266), elementwise code short enough for the
+// instruction cache and the first S ahead of V and dO (-> 248; either alone
+// gained nothing), dV before dS and S, D in turn (-> 243).  Four elementwise
+// groups of 32 columns: 253; V released early in longer code: 309.
 //
 // Every mbarrier wait is bounded; on expiry the CTA drains its copies and
 // MMAs in flight, frees TMEM and returns.
