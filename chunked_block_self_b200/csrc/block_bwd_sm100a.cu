@@ -9,7 +9,7 @@
 // unit = (key tile, 64 queries): with rows = keys and columns = queries
 //     S = K_c Q_u^T,  D = V_c dO_u^T          (M = 128, N <= 64, K = 64)
 //     P = exp2(S s log2e - lse log2e), dS = P (D - delta)   (elementwise)
-//     dV_c += P dO_u     A = P in TMEM (over S), B = dO rows
+//     dV_c += P dO_u     A = P in TMEM (over D), B = dO rows
 //     dK_c += dS Q_u     A = dS in shared memory, K-major, B = Q rows
 //     dQ_x += dS^T K_c   A = the same shared memory read M-major: 128 queries
 //                        (two units), K = the tile's keys, B = K rows
@@ -39,14 +39,14 @@
 // at 1.8 k each, two in flight: the elementwise work of one is about 2 k (512
 // for its exps), the hops between its warps and the issue of its MMAs as much
 // again, the tensor pipe busy for 0.9 k.  HBM would allow 8 k.  The batch of
-// 128 utterances (16 heads, 58,903 frames, 5,648 blocks): 0.36 ms, and 0.04 ms
-// for delta: 2.4 TB/s of the operator's bytes.  Steps that paid: three
-// warpgroups' registers without spills (388 -> 293 us on a batch of 34,512
-// frames; beside 200 KB of shared memory a spill lives in L2), results on warps
-// of their own and S ahead (-> 266), elementwise code short enough for the
-// instruction cache and the first S ahead of V and dO (-> 248; either alone
-// gained nothing), dV before dS and S, D in turn (-> 243).  Four elementwise
-// groups of 32 columns: 253; V released early in longer code: 309.
+// 128 utterances (16 heads, 58,903 frames, 5,648 items): 0.36 ms, and 0.04 ms
+// for delta: 2.4 TB/s of the operator's bytes.  Steps that paid, on a batch of
+// 34,512 frames: no spilled registers (388 -> 293 us; beside 200 KB of shared
+// memory a spill lives in L2), results on warps of their own and S ahead
+// (-> 266), elementwise code short enough for the instruction cache and the
+// first S ahead of V and dO (-> 248; alone 262 and 309), dV before dS and S, D
+// in turn (-> 243).  Four elementwise groups of 32 columns: 253; delta formed
+// here by four more warps: 260.
 //
 // Every mbarrier wait is bounded; on expiry the CTA drains its copies and
 // MMAs in flight, frees TMEM and returns.
