@@ -342,8 +342,11 @@ __device__ __forceinline__ void backward_heads(const Rows &r, long long f, const
         for (int b = 0; b < kBwdBatch; ++b) {
             const int h = h0 + 4 * b + hg;
             const bool in = h < r.heads;
+            // past the last head dy = 0 and x = 1: r is finite whatever eps
+            // (0 * r of a zero row with eps = 0 would be NaN), dw gets 0
             dy[b] = in ? *reinterpret_cast<const uint4 *>(src + (long long)h * 128) : make_uint4(0, 0, 0, 0);
-            xx[b] = in ? *reinterpret_cast<const uint4 *>(xs + (long long)h * 128) : make_uint4(0, 0, 0, 0);
+            xx[b] = in ? *reinterpret_cast<const uint4 *>(xs + (long long)h * 128)
+                       : make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
         }
 #pragma unroll
         for (int b = 0; b < kBwdBatch; ++b) {
@@ -369,7 +372,6 @@ __device__ __forceinline__ void backward_heads(const Rows &r, long long f, const
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 dx.v[e] = rr * (dz.v[e] * ww.v[e] - x.v[e] * m);
-                // rows past the last head hold zeros: no contribution
                 dw[e] = fmaf(dz.v[e], x.v[e] * rr, dw[e]);
             }
             if (h < r.heads)

@@ -351,3 +351,23 @@ def test_heads_beyond_one_batch(cuda_device):
         _check_fwd(ko, x["k"], x["wk"], pos, f, inter=inter)
         _check_bwd(gq, gwq, x["dq"], x["q"], x["wq"], pos, f, inter=inter)
         _check_bwd(gk, gwk, x["dk"], x["k"], x["wk"], pos, f, inter=inter)
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("heads", [1, 3, 5, 17])
+def test_gradient_without_eps(heads, inter, cuda_device):
+    """eps = 0 and head counts that are no multiples of four: a lane without a
+    head has a zero row, whose r is infinite, and must add nothing to the
+    weights' gradients."""
+    nle = _nle()
+    x = _draw([21, 2], heads, 2, 23 + heads)
+    d = _dev(x, cuda_device)
+    f = _freq(32)
+    ft = torch.from_numpy(f).to(cuda_device)
+    qo, ko = nle.qk_norm_rope(d["q"], d["k"], d["cu"], ft, d["wq"], d["wk"], eps=0.0, interleaved=inter)
+    gq, gk, gwq, gwk = nle.qk_norm_rope_bwd(d["dq"], d["dk"], d["cu"], ft, d["q"], d["k"], d["wq"], d["wk"], eps=0.0,
+                                            interleaved=inter)
+    pos = rope.positions(x["cu"])
+    for y, g, gw, n in ((qo, gq, gwq, "q"), (ko, gk, gwk, "k")):
+        _check_fwd(y, x[n], x["w" + n], pos, f, eps=0.0, inter=inter)
+        _check_bwd(g, gw, x["d" + n], x[n], x["w" + n], pos, f, eps=0.0, inter=inter)
