@@ -205,7 +205,10 @@ __device__ __forceinline__ Factors factors(const Turn<kInter> &u, const uint4 &w
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             f.a[e] *= ww.v[e];
-            f.b[e] *= kInter ? ww.v[e ^ 1] : pw.v[e];
+            if (!kInter)   // an unrotated chunk is its own partner
+                f.b[e] *= pw.v[e];
+            else if (rotated)
+                f.b[e] *= ww.v[e ^ 1];
         }
     }
     return f;
@@ -251,7 +254,9 @@ __device__ __forceinline__ void forward_heads(const Rows &r, long long f, const 
             Chunk y;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                y.v[e] = fmaf(u.b[e], xp.v[kInter ? e ^ 1 : e], u.a[e] * x.v[e]);
+                // unrotated elements take nothing of their neighbour: 0 * Inf is NaN
+                const float xo = !kInter ? xp.v[e] : !kNorm || l.rotated ? x.v[e ^ 1] : 0.f;
+                y.v[e] = fmaf(u.b[e], xo, u.a[e] * x.v[e]);
                 if (kNorm)
                     y.v[e] *= rr;
             }

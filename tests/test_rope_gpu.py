@@ -371,3 +371,30 @@ def test_gradient_without_eps(heads, inter, cuda_device):
     for y, g, gw, n in ((qo, gq, gwq, "q"), (ko, gk, gwk, "k")):
         _check_fwd(y, x[n], x["w" + n], pos, f, eps=0.0, inter=inter)
         _check_bwd(g, gw, x["d" + n], x[n], x["w" + n], pos, f, eps=0.0, inter=inter)
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("rot", [0, 16, 32, 48])
+def test_norm_of_rows_with_infinities_past_the_rotation(rot, inter, cuda_device):
+    """An infinity makes the row's r zero: the element itself becomes NaN
+    (Inf * 0) and every other one zero, its neighbour too where pairs are
+    neighbours.  A NaN among the weights past rot_dim reaches its own element
+    of every row and no other."""
+    nle = _nle()
+    x = _draw([9], 2, 3, 31 + rot)
+    x["q"][2, 1, 50] = float("inf")
+    x["q"][3, 0, 51] = -float("inf")
+    d = _dev(x, cuda_device)
+    ft = torch.from_numpy(_freq(rot)).to(cuda_device) if rot else None
+    bad = d["wk"].clone()
+    bad[53] = float("nan")
+    _, want = nle.qk_norm_rope(d["q"], d["k"], d["cu"], ft, d["wq"], d["wk"], interleaved=inter)
+    qo, ko = nle.qk_norm_rope(d["q"], d["k"], d["cu"], ft, d["wq"], bad, interleaved=inter)
+    for f, h, e in ((2, 1, 50), (3, 0, 51)):
+        row = qo[f, h].clone()
+        assert torch.isnan(row[e])
+        row[e] = 0
+        assert (row == 0).all(), torch.nonzero(row != 0).flatten().tolist()
+    assert torch.isnan(ko[..., 53]).all()
+    keep = [e for e in range(64) if e != 53]
+    assert torch.equal(ko[..., keep], want[..., keep])
