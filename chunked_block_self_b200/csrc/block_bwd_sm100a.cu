@@ -531,6 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             ok = false;
                             break;
                         }
+                        tc_fence_after();
                         if (elect_one()) {
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
