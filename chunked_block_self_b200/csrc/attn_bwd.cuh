@@ -124,12 +124,17 @@ __device__ __forceinline__ void store_rows(const uint32_t (&o)[16], __nv_bfloat1
     }
 }
 
+// delta[h][f] = sum_d dout_fhd out_fhd of every frame, into the workspace.
+int launch_attn_delta(const void *out, const void *dout, float *delta, int64_t total, int heads, const DeviceInfo &di,
+                      cudaStream_t st);
+
 // The gradient of block attention, whole blocks at a time
-// (block_bwd_sm100a.cu), after delta has been computed; items: an upper bound
-// of the (block, head) pairs.
+// (block_bwd_sm100a.cu): delta and the gradient, launched once all of its own
+// checks have passed; items: an upper bound of the (block, head) pairs.
 struct BlockBwdArgs {
-    const void *q, *k, *v, *dout;
-    const float *lse, *delta;
+    const void *q, *k, *v, *out, *dout;
+    const float *lse;
+    float *delta;
     void *dq, *dk, *dv;
     const int32_t *cu;
     int32_t *status;

@@ -726,47 +726,11 @@ int launch_attn_bwd(const nle_attn_bwd_args *a, int block, void *stream)
     if ((items / grid + 1) * ((block ? block : a->total_frames) / kTile + 1) > 0x7fffffffLL)
         return NLE_ERR_UNSUPPORTED;
 
-    Params p{};
-    p.cu = a->cu_seqlens;
-    p.n_seq = a->n_seq;
-    p.total = (int)a->total_frames;
-    p.heads = a->heads;
-    p.block = block;
-    p.xtiles = xtiles;
-    // above half the SM's: one CTA per SM (it owns all TMEM)
-    const size_t smem = kBarsOff + ((sizeof(Bars) + 127) / 128) * 128 + 1024;
-    if (smem > (size_t)di.smem_optin)
-        return NLE_ERR_UNSUPPORTED;
     const double scale = a->softmax_scale > 0.f ? (double)a->softmax_scale : 1.0 / std::sqrt((double)a->d_head);
-    p.scale = (float)scale;
-    p.scale_log2 = (float)(scale * 1.4426950408889634);
-    p.lse = a->lse;
-    p.delta = static_cast<const float *>(a->workspace);
-    p.dq = static_cast<__nv_bfloat16 *>(a->dq);
-    p.dk = static_cast<__nv_bfloat16 *>(a->dk);
-    p.dv = static_cast<__nv_bfloat16 *>(a->dv);
-    p.out_stride = dstride;
-    p.status = a->dev_status;
-    p.wait_ns = a->wait_limit_ns > 0 ? (unsigned long long)a->wait_limit_ns : 1000000000ull;
-    p.flags = a->flags;
-
-    CUtensorMap tq, tk, tv, tdo;
-    const uint64_t cols = (uint64_t)dense, rows = (uint64_t)a->total_frames;
-    if (!nle::encode_tmap_bf16_2d(&tq, a->q, cols, rows, stride, 64, kTile) ||
-        !nle::encode_tmap_bf16_2d(&tk, a->k, cols, rows, stride, 64, kTile) ||
-        !nle::encode_tmap_bf16_2d(&tv, a->v, cols, rows, stride, 64, kTile) ||
-        !nle::encode_tmap_bf16_2d(&tdo, a->dout, cols, rows, dense, 64, kTile))
-        return NLE_ERR_CUDA;
-    if (!nle::allow_max_dynamic_smem(reinterpret_cast<const void *>(attn_bwd_kernel), dev, di.smem_optin))
-        return NLE_ERR_CUDA;
+    const float scale_log2 = (float)(scale * 1.4426950408889634);
+    float *delta = static_cast<float *>(a->workspace);
+    const unsigned long long wait_ns = a->wait_limit_ns > 0 ? (unsigned long long)a->wait_limit_ns : 1000000000ull;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const long long drows = a->total_frames * (long long)a->heads;
-    const long long dgrid = (drows + 31) / 32;
-    attn_delta_kernel<<<(unsigned)(dgrid < 16ll * di.sm_count ? dgrid : 16ll * di.sm_count), 256, 0, st>>>(
-        static_cast<const uint4 *>(a->out), static_cast<const uint4 *>(a->dout), dense,
-        static_cast<float *>(a->workspace), p.total, a->heads);
-    if (cudaGetLastError() != cudaSuccess)
-        return NLE_ERR_CUDA;
     // Blocks of more than one key tile, and at least one (block, head) per SM:
     // whole blocks on chip (batch of 128 utterances: 395 us against 491 us here,
     // with delta's 41 us in both).  One key tile leaves that kernel's second half
@@ -779,9 +743,10 @@ int launch_attn_bwd(const nle_attn_bwd_args *a, int block, void *stream)
         b.q = a->q;
         b.k = a->k;
         b.v = a->v;
+        b.out = a->out;
         b.dout = a->dout;
         b.lse = a->lse;
-        b.delta = p.delta;
+        b.delta = delta;
         b.dq = a->dq;
         b.dk = a->dk;
         b.dv = a->dv;
@@ -793,17 +758,67 @@ int launch_attn_bwd(const nle_attn_bwd_args *a, int block, void *stream)
         b.n_seq = a->n_seq;
         b.heads = a->heads;
         b.block = block;
-        b.scale = p.scale;
-        b.scale_log2 = p.scale_log2;
-        b.wait_ns = p.wait_ns;
+        b.scale = (float)scale;
+        b.scale_log2 = scale_log2;
+        b.wait_ns = wait_ns;
         b.flags = a->flags;
         return nle::launch_block_bwd(b, di, dev, units * a->heads, st);
     }
+
+    Params p{};
+    p.cu = a->cu_seqlens;
+    p.n_seq = a->n_seq;
+    p.total = (int)a->total_frames;
+    p.heads = a->heads;
+    p.block = block;
+    p.xtiles = xtiles;
+    // above half the SM's: one CTA per SM (it owns all TMEM)
+    const size_t smem = kBarsOff + ((sizeof(Bars) + 127) / 128) * 128 + 1024;
+    if (smem > (size_t)di.smem_optin)
+        return NLE_ERR_UNSUPPORTED;
+    p.scale = (float)scale;
+    p.scale_log2 = scale_log2;
+    p.lse = a->lse;
+    p.delta = delta;
+    p.dq = static_cast<__nv_bfloat16 *>(a->dq);
+    p.dk = static_cast<__nv_bfloat16 *>(a->dk);
+    p.dv = static_cast<__nv_bfloat16 *>(a->dv);
+    p.out_stride = dstride;
+    p.status = a->dev_status;
+    p.wait_ns = wait_ns;
+    p.flags = a->flags;
+
+    CUtensorMap tq, tk, tv, tdo;
+    const uint64_t cols = (uint64_t)dense, rows = (uint64_t)a->total_frames;
+    if (!nle::encode_tmap_bf16_2d(&tq, a->q, cols, rows, stride, 64, kTile) ||
+        !nle::encode_tmap_bf16_2d(&tk, a->k, cols, rows, stride, 64, kTile) ||
+        !nle::encode_tmap_bf16_2d(&tv, a->v, cols, rows, stride, 64, kTile) ||
+        !nle::encode_tmap_bf16_2d(&tdo, a->dout, cols, rows, dense, 64, kTile))
+        return NLE_ERR_CUDA;
+    if (!nle::allow_max_dynamic_smem(reinterpret_cast<const void *>(attn_bwd_kernel), dev, di.smem_optin))
+        return NLE_ERR_CUDA;
+    const int rc = nle::launch_attn_delta(a->out, a->dout, delta, a->total_frames, a->heads, di, st);
+    if (rc != NLE_OK)
+        return rc;
     attn_bwd_kernel<<<grid, kThreads, smem, st>>>(tq, tk, tv, tdo, p);
     return cudaGetLastError() == cudaSuccess ? NLE_OK : NLE_ERR_CUDA;
 }
 
 } // namespace
+
+namespace nle {
+
+int launch_attn_delta(const void *out, const void *dout, float *delta, int64_t total, int heads, const DeviceInfo &di,
+                      cudaStream_t st)
+{
+    const long long grid = (total * heads + 31) / 32, most = 16ll * di.sm_count;
+    attn_delta_kernel<<<(unsigned)(grid < most ? grid : most), 256, 0, st>>>(
+        static_cast<const uint4 *>(out), static_cast<const uint4 *>(dout), (long long)heads * 64, delta, (int)total,
+        heads);
+    return cudaGetLastError() == cudaSuccess ? NLE_OK : NLE_ERR_CUDA;
+}
+
+} // namespace nle
 
 extern "C" int nle_block_attn_bwd(const nle_attn_bwd_args *args, int block_frames, void *stream)
 {

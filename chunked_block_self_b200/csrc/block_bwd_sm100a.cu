@@ -785,6 +785,9 @@ int launch_block_bwd(const BlockBwdArgs &a, const DeviceInfo &di, int dev, long 
         return NLE_ERR_CUDA;
     if (!allow_max_dynamic_smem(reinterpret_cast<const void *>(block_bwd_kernel), dev, di.smem_optin))
         return NLE_ERR_CUDA;
+    const int rc = launch_attn_delta(a.out, a.dout, a.delta, a.total, a.heads, di, st);
+    if (rc != NLE_OK)
+        return rc;
     const int grid = (int)(items < di.sm_count ? items : di.sm_count);
     block_bwd_kernel<<<grid, kThreads, smem, st>>>(tq, tk, tv, tdo, p);
     return cudaGetLastError() == cudaSuccess ? NLE_OK : NLE_ERR_CUDA;
