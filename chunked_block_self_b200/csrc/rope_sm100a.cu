@@ -467,6 +467,27 @@ int check_rows(const void *ptr, int64_t *stride, int heads)
     return NLE_OK;
 }
 
+// A buffer of a call.  tensor: 0 (q), 1 (k): the sources and the output of
+// one tensor, which may be one buffer (at one stride); -1: of its own.
+struct Buffer {
+    const void *p;
+    int tensor;
+    bool written;
+};
+
+// Does anything written begin where another buffer does?
+template <int n>
+bool written_twice(const Buffer (&b)[n])
+{
+    for (int i = 0; i < n; ++i)
+        for (int j = 0; j < i; ++j) {
+            const bool own = b[i].tensor >= 0 && b[i].tensor == b[j].tensor && b[i].written != b[j].written;
+            if (b[i].p && b[i].p == b[j].p && (b[i].written || b[j].written) && !own)
+                return true;
+        }
+    return false;
+}
+
 // Shared checks of the two entry points; *work: there is something to do.
 int check_plan(const nle_rope_plan *r, bool *work)
 {
@@ -576,6 +597,10 @@ extern "C" int nle_qk_norm_rope_fwd(const nle_rope_plan *plan, const void *q, in
         r.heads = t[i].heads;
         r.w = static_cast<const __nv_bfloat16 *>(t[i].w);
     }
+    if (written_twice<10>({{p.q.src, 0, false}, {p.k.src, 1, false}, {p.q.dst, 0, true}, {p.k.dst, 1, true},
+                           {plan->q_weight, -1, false}, {plan->k_weight, -1, false}, {plan->inv_freq, -1, false},
+                           {plan->cu_seqlens, -1, false}, {plan->positions, -1, false}, {plan->dev_status, -1, false}}))
+        return NLE_ERR_INVALID_ARG;
     nle::DeviceInfo di;
     if ((rc = fill_params(plan, &p, &di)) != NLE_OK)
         return rc;
@@ -622,7 +647,8 @@ extern "C" int nle_qk_norm_rope_bwd(const nle_rope_plan *plan, const void *dq_ou
             (norm && (rc = check_rows(t[i].x, &t[i].xs, t[i].heads)) != NLE_OK) ||
             (rc = check_rows(t[i].dst, &t[i].ds, t[i].heads)) != NLE_OK)
             return rc;
-        if (t[i].src == t[i].dst && t[i].ss != t[i].ds)   // in place: the same frames
+        if ((t[i].src == t[i].dst && t[i].ss != t[i].ds) ||   // in place: the same frames
+            (norm && t[i].x == t[i].dst && t[i].xs != t[i].ds))
             return NLE_ERR_INVALID_ARG;
         Rows &r = i ? p.k : p.q;
         r.src = static_cast<const uint8_t *>(t[i].src);
@@ -638,6 +664,13 @@ extern "C" int nle_qk_norm_rope_bwd(const nle_rope_plan *plan, const void *dq_ou
         return NLE_ERR_INVALID_ARG;
     if (norm && !nle::aligned16(workspace))
         return NLE_ERR_MISALIGNED;
+    if (written_twice<15>({{p.q.src, 0, false}, {p.k.src, 1, false}, {norm ? p.q.x : nullptr, 0, false},
+                           {norm ? p.k.x : nullptr, 1, false}, {p.q.dst, 0, true}, {p.k.dst, 1, true},
+                           {norm ? dq_weight : nullptr, -1, true}, {norm ? dk_weight : nullptr, -1, true},
+                           {norm ? workspace : nullptr, -1, true}, {plan->q_weight, -1, false},
+                           {plan->k_weight, -1, false}, {plan->inv_freq, -1, false}, {plan->cu_seqlens, -1, false},
+                           {plan->positions, -1, false}, {plan->dev_status, -1, false}}))
+        return NLE_ERR_INVALID_ARG;
     nle::DeviceInfo di;
     if ((rc = fill_params(plan, &p, &di)) != NLE_OK)
         return rc;

@@ -332,11 +332,14 @@ int nle_varlen_attn_bwd(const nle_attn_bwd_args *args, void *stream);
  * least heads * 64), so that they may lie inside a fused projection buffer.
  *
  * nle_qk_norm_rope_fwd: q_out, k_out from q, k.  An output may be its input
- * (same pointer and stride); other overlaps are not allowed.
+ * (same pointer and stride); other overlaps are not allowed, and an output
+ * that begins where another buffer does is NLE_ERR_INVALID_ARG.
  * nle_qk_norm_rope_bwd: from the gradients dq_out, dk_out of the outputs and
  * (read only with weights; may be NULL without) the inputs q, k: dq, dk, and
  * the weights' gradients dq_weight, dk_weight: nullable float [64], written,
- * not accumulated.  dq may be dq_out and dk dk_out.  workspace: with weights,
+ * not accumulated.  dq may be dq_out or q, and dk dk_out or k (same pointer and
+ * stride); other overlaps of dq, dk, the weights' gradients and the workspace
+ * are not allowed, as in the forward.  workspace: with weights,
  * NLE_ROPE_BWD_WORKSPACE_BYTES of device scratch, 16-byte aligned, used by
  * this call alone until it has run; its content need not be kept.  Results
  * are the same bits on every call.

@@ -398,3 +398,25 @@ def test_norm_of_rows_with_infinities_past_the_rotation(rot, inter, cuda_device)
     assert torch.isnan(ko[..., 53]).all()
     keep = [e for e in range(64) if e != 53]
     assert torch.equal(ko[..., keep], want[..., keep])
+
+
+def test_gradient_over_its_inputs_and_refused_overlaps(cuda_device):
+    """dq and dk may be written over q and k; an output that begins at another
+    output or at the other tensor is refused."""
+    nle = _nle()
+    x = _draw([70, 13], 37, 3, 41)
+    d = _dev(x, cuda_device)
+    ft = torch.from_numpy(_freq(64)).to(cuda_device)
+    rest = (d["cu"], ft)
+    ref = nle.qk_norm_rope_bwd(d["dq"], d["dk"], *rest, d["q"], d["k"], d["wq"], d["wk"])
+    q, k = d["q"].clone(), d["k"].clone()
+    got = nle.qk_norm_rope_bwd(d["dq"], d["dk"], *rest, q, k, d["wq"], d["wk"], out=(q, k))
+    assert all(torch.equal(a, b) for a, b in zip(got, ref))
+    # three heads each, so that either tensor's shape fits
+    a, b, c = d["k"], d["dk"], torch.empty_like(d["k"])
+    for out in ((c, c), (b, c), (c, a), (b, a)):
+        with pytest.raises(nle.NLEError):
+            nle.qk_norm_rope(a, b, *rest, d["wq"], d["wk"], out=out)
+    for out in ((c, c), (b, c), (c, a)):
+        with pytest.raises(nle.NLEError):
+            nle.qk_norm_rope_bwd(a, b, *rest, torch.empty_like(a), torch.empty_like(a), d["wq"], d["wk"], out=out)

@@ -142,3 +142,52 @@ def test_binding_refusals():
         nle.qk_norm_rope(None, None, cu, None)
     with pytest.raises(ValueError):
         nle.qk_norm_rope_bwd(None, None, cu, None)
+
+
+_NAMES = ("q", "k", "q_weight", "k_weight", "inv_freq", "cu_seqlens", "positions", "dev_status")
+_FWD_OUT = ("q_out", "k_out")
+_BWD_OUT = ("dq_out", "dk_out", "dq", "dk", "dq_weight", "dk_weight", "workspace")   # and the gradients read
+
+
+def _distinct(outputs, **kw):
+    """A call's buffers at addresses of their own (plan fields among them)."""
+    a = {n: 4096 * (i + 1) for i, n in enumerate(_NAMES + outputs)}
+    a.update(kw)
+    return a, _plan(**{n: a[n] for n in _NAMES[2:]})
+
+
+def _fwd_at(**kw):
+    a, p = _distinct(_FWD_OUT, **kw)
+    return nle._lib.nle_qk_norm_rope_fwd(ctypes.byref(p), a["q"], a.get("qs", 0), a["k"], 0, a["q_out"],
+                                         a.get("qos", 0), a["k_out"], 0, None)
+
+
+def _bwd_at(**kw):
+    a, p = _distinct(_BWD_OUT, **kw)
+    return nle._lib.nle_qk_norm_rope_bwd(ctypes.byref(p), a["dq_out"], 0, a["dk_out"], 0, a["q"], a.get("qs", 0),
+                                         a["k"], 0, a["dq"], a.get("qos", 0), a["dk"], 0, a["dq_weight"],
+                                         a["dk_weight"], a["workspace"], None)
+
+
+@pytest.mark.parametrize("f,written,own", [
+    (_fwd_at, ("q_out", "k_out"), {("q_out", "q"), ("k_out", "k")}),
+    (_bwd_at, ("dq", "dk", "dq_weight", "dk_weight", "workspace"),
+     {("dq", "dq_out"), ("dq", "q"), ("dk", "dk_out"), ("dk", "k")})])
+def test_outputs_that_begin_at_another_buffer(f, written, own):
+    """Refused wherever an output begins at another output or at any buffer that
+    is read, but its own tensor's source at the same stride; without them the
+    call gets as far as the device (no status of the argument checks)."""
+    checks = (nle.NLE_ERR_INVALID_ARG, nle.NLE_ERR_MISALIGNED)
+    a, _ = _distinct(_FWD_OUT if f is _fwd_at else _BWD_OUT)
+    if not torch.cuda.is_available():   # with a device a good call would launch on these addresses
+        assert f() not in checks
+        for n, m in own:
+            assert f(**{n: a[m]}) not in checks, (n, m)
+    for n in written:
+        for m in a:
+            if m != n and (n, m) not in own:
+                assert f(**{n: a[m]}) == nle.NLE_ERR_INVALID_ARG, (n, m)
+    # its own source, frames apart by another stride
+    n, m = ("q_out", "q") if f is _fwd_at else ("dq", "q")
+    assert f(**{n: a[m], "qs": 9 * 64}) == nle.NLE_ERR_INVALID_ARG
+    assert f(**{n: a[m], "qos": 9 * 64}) == nle.NLE_ERR_INVALID_ARG
