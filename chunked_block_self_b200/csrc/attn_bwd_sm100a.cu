@@ -707,6 +707,8 @@ int launch_attn_bwd(const nle_attn_bwd_args *a, int block, void *stream)
     for (int i = 8; i < 11; ++i)
         if (!nle::aligned4(ptrs[i]))
             return NLE_ERR_MISALIGNED;
+    if (!nle::aligned4(a->dev_status))
+        return NLE_ERR_MISALIGNED;
     // what is written (dq, dk, dv, workspace) begins at no other buffer's start
     for (int i = 5; i < 11; ++i)
         for (int j = 0; j < i; ++j)

@@ -593,7 +593,7 @@ int launch_block_attn(const void *q, const void *k, const void *v, void *out, fl
     if (stride < dense || dense > 0x7fffffffLL)
         return NLE_ERR_INVALID_ARG;
     if (stride % 8 != 0 || !nle::aligned16(q) || !nle::aligned16(k) || !nle::aligned16(v) ||
-        !nle::aligned16(out) || !nle::aligned4(lse))
+        !nle::aligned16(out) || !nle::aligned4(lse) || (lse && !nle::aligned4(dev_status)))
         return NLE_ERR_MISALIGNED;
 
     nle::DeviceInfo di;

@@ -508,7 +508,7 @@ int check_plan(const nle_rope_plan *r, bool *work)
         return NLE_ERR_INVALID_ARG;
     if ((r->q_weight && !nle::aligned16(r->q_weight)) || (r->k_weight && !nle::aligned16(r->k_weight)))
         return NLE_ERR_MISALIGNED;
-    if (!nle::aligned4(r->cu_seqlens) || !nle::aligned4(r->positions) ||
+    if (!nle::aligned4(r->cu_seqlens) || !nle::aligned4(r->positions) || !nle::aligned4(r->dev_status) ||
         (r->rot_dim > 0 && (reinterpret_cast<uintptr_t>(r->inv_freq) & 7)))
         return NLE_ERR_MISALIGNED;
     *work = true;
@@ -662,7 +662,7 @@ extern "C" int nle_qk_norm_rope_bwd(const nle_rope_plan *plan, const void *dq_ou
     }
     if (norm && !workspace)
         return NLE_ERR_INVALID_ARG;
-    if (norm && !nle::aligned16(workspace))
+    if (norm && (!nle::aligned16(workspace) || !nle::aligned4(dq_weight) || !nle::aligned4(dk_weight)))
         return NLE_ERR_MISALIGNED;
     if (written_twice<15>({{p.q.src, 0, false}, {p.k.src, 1, false}, {norm ? p.q.x : nullptr, 0, false},
                            {norm ? p.k.x : nullptr, 1, false}, {p.q.dst, 0, true}, {p.k.dst, 1, true},

@@ -231,7 +231,8 @@ int nle_varlen_attn_fwd_ex(const void *q, const void *k, const void *v, void *ou
  * Training forms of block attention and of full-utterance attention: the
  * forward pass that also keeps every row's log-sum-exp, and the gradient.
  *
- * nle_*_fwd_lse: as the _ex form (the same out, bit for bit), plus
+ * nle_*_fwd_lse: as the _ex form (the same out, bit for bit; dev_status 4-byte
+ * aligned), plus
  * lse  device float [heads][total_frames], out:
  *      lse[h][i] = ln sum_j exp(softmax_scale * q_i.k_j) over the frames j
  *      that frame i attends to (natural log); 4-byte aligned.  Entries of
@@ -326,7 +327,7 @@ int nle_varlen_attn_bwd(const nle_attn_bwd_args *args, void *stream);
  *   rot_dim      0, 16, 32, 48 or 64
  *   interleaved  0 or 1
  *   rot_scale    0 selects 1
- *   dev_status   nullable int32: receives NLE_ERR_INVALID_ARG
+ *   dev_status   nullable int32, 4-byte aligned: receives NLE_ERR_INVALID_ARG
  * Tensors are bf16 [total_frames][heads][64], 16-byte aligned; each *_stride
  * is the elements between its frames (0: heads * 64; a multiple of 8, at
  * least heads * 64), so that they may lie inside a fused projection buffer.
@@ -336,8 +337,8 @@ int nle_varlen_attn_bwd(const nle_attn_bwd_args *args, void *stream);
  * that begins where another buffer does is NLE_ERR_INVALID_ARG.
  * nle_qk_norm_rope_bwd: from the gradients dq_out, dk_out of the outputs and
  * (read only with weights; may be NULL without) the inputs q, k: dq, dk, and
- * the weights' gradients dq_weight, dk_weight: nullable float [64], written,
- * not accumulated.  dq may be dq_out or q, and dk dk_out or k (same pointer and
+ * the weights' gradients dq_weight, dk_weight: nullable float [64], 4-byte
+ * aligned, written, not accumulated.  dq may be dq_out or q, and dk dk_out or k (same pointer and
  * stride); other overlaps of dq, dk, the weights' gradients and the workspace
  * are not allowed, as in the forward.  workspace: with weights,
  * NLE_ROPE_BWD_WORKSPACE_BYTES of device scratch, 16-byte aligned, used by

@@ -144,3 +144,15 @@ def test_binding_rejects_cpu_tensors():
     for f in (nle.block_attn_bwd, nle.varlen_attn_bwd):
         with pytest.raises(TypeError):
             f(x, x, x, x, x, lse, cu)
+
+
+def test_status_off_its_alignment():
+    """dev_status is written by an atomic: 4-byte aligned, as the other small buffers."""
+    a = {n: 1024 * (i + 1) for i, n in enumerate(("q", "k", "v", "out", "dout", "lse", "cu_seqlens", "dq", "dk", "dv",
+                                                  "workspace"))}
+    for f in (_block, _varlen):
+        assert f(**a, dev_status=18) == nle.NLE_ERR_MISALIGNED
+    f = nle._lib.nle_block_attn_fwd_lse
+    assert f(16, 16, 16, 48, 64, 16, 1, 400, 8, 64, 200, 0.0, 0, 18, 0, 0, None) == nle.NLE_ERR_MISALIGNED
+    f = nle._lib.nle_varlen_attn_fwd_lse
+    assert f(16, 16, 16, 48, 64, 16, 1, 400, 8, 64, 0.0, 0, 18, 0, 0, None) == nle.NLE_ERR_MISALIGNED

@@ -191,3 +191,9 @@ def test_outputs_that_begin_at_another_buffer(f, written, own):
     n, m = ("q_out", "q") if f is _fwd_at else ("dq", "q")
     assert f(**{n: a[m], "qs": 9 * 64}) == nle.NLE_ERR_INVALID_ARG
     assert f(**{n: a[m], "qos": 9 * 64}) == nle.NLE_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("f,names", [(_fwd_at, ("dev_status",)), (_bwd_at, ("dq_weight", "dk_weight", "dev_status"))])
+def test_pointers_off_their_alignment(f, names):
+    for n in names:
+        assert f(**{n: (1 << 20) + 2}) == nle.NLE_ERR_MISALIGNED, n
