@@ -385,9 +385,9 @@ def _rows(t, name: str, frames: int | None = None, index: int | None = None) -> 
     return rows
 
 
-def _small(t, name: str, dtype, numel: int, index: int) -> None:
-    """Checks an optional contiguous CUDA tensor of `numel` elements (-1: any)."""
-    if t is None:
+def _small(t, name: str, dtype, numel: int, index: int, optional: bool = True) -> None:
+    """Checks a contiguous CUDA tensor of `numel` elements (-1: any), which may be None if it is optional."""
+    if t is None and optional:
         return
     _dev_tensor(t, name, dtype)
     if not t.is_contiguous() or (numel >= 0 and t.numel() != numel):
@@ -397,7 +397,7 @@ def _small(t, name: str, dtype, numel: int, index: int) -> None:
 
 
 def _n_seq(cu_seqlens, index: int) -> int:
-    _small(cu_seqlens, "cu_seqlens", torch.int32, -1, index)
+    _small(cu_seqlens, "cu_seqlens", torch.int32, -1, index, optional=False)
     if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
         raise ValueError("cu_seqlens: [n_seq + 1] required")
     return cu_seqlens.numel() - 1
@@ -563,7 +563,7 @@ def _attn_bwd(dout, q, k, v, out, lse, cu_seqlens, block_frames, softmax_scale, 
     frames, heads = shape[0], shape[1]
     _dense(dout, "dout", shape, index)
     _dense(out, "out", shape, index)
-    _small(lse, "lse", torch.float32, heads * frames, index)
+    _small(lse, "lse", torch.float32, heads * frames, index, optional=False)
     if lse.shape != (heads, frames):
         raise ValueError(f"lse: [{heads}, {frames}] required")
     n_seq = _n_seq(cu_seqlens, index)

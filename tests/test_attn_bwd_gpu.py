@@ -393,3 +393,17 @@ def test_layer_chain_forward_and_gradient(block, cuda_device):
     rdk, rwk, _ = rope.norm_rope_bwd(g[1], k64, _np(wk), pos, fr)
     for got, want in ((out, o64), (dq, rdq), (dk, rdk), (dv, g[2]), (gwq, rwq), (gwk, rwk)):
         assert np.linalg.norm(_np(got) - want) <= 5 * 2.0 ** -8 * np.linalg.norm(want)
+
+
+@pytest.mark.parametrize("f", ["block_attn", "varlen_attn"])
+def test_missing_tensors_are_named(f, cuda_device):
+    nle = _nle()
+    x = _inputs([30], 2, 98)
+    fwd, bwd = getattr(nle, f + "_lse"), getattr(nle, f + "_bwd")
+    out, lse = fwd(x["q"], x["k"], x["v"], x["cud"])
+    with pytest.raises(TypeError, match="cu_seqlens"):
+        fwd(x["q"], x["k"], x["v"], None)
+    args = dict(dout=x["dout"], q=x["q"], k=x["k"], v=x["v"], out=out, lse=lse, cu_seqlens=x["cud"])
+    for n in args:
+        with pytest.raises(TypeError, match=n):
+            bwd(**dict(args, **{n: None}))

@@ -156,3 +156,8 @@ def test_status_off_its_alignment():
     assert f(16, 16, 16, 48, 64, 16, 1, 400, 8, 64, 200, 0.0, 0, 18, 0, 0, None) == nle.NLE_ERR_MISALIGNED
     f = nle._lib.nle_varlen_attn_fwd_lse
     assert f(16, 16, 16, 48, 64, 16, 1, 400, 8, 64, 0.0, 0, 18, 0, 0, None) == nle.NLE_ERR_MISALIGNED
+
+
+def test_binding_names_missing_offsets():
+    with pytest.raises(TypeError, match="cu_seqlens must be a CUDA tensor"):
+        nle._n_seq(None, 0)
