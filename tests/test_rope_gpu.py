@@ -420,3 +420,52 @@ def test_gradient_over_its_inputs_and_refused_overlaps(cuda_device):
     for out in ((c, c), (b, c), (c, a)):
         with pytest.raises(nle.NLEError):
             nle.qk_norm_rope_bwd(a, b, *rest, torch.empty_like(a), torch.empty_like(a), d["wq"], d["wk"], out=out)
+
+
+def _check_dw(got, dy, x, w, pos, f, units, frames, heads, inter, dev):
+    """The weights' gradient against the definition, under the bound of the
+    kernel's own chain: a CTA's warp adds a frame of each of its units of 8
+    frames, ceil(heads / 4) terms a lane, then 2 steps of a shuffle and the
+    CTA's 8 warps in fp32 (the CTAs in fp64, rounded once); a term's own error
+    is below 32 * 2^-24."""
+    grid = min(frames // 8 + 5, 2 * torch.cuda.get_device_properties(dev).multi_processor_count, 2048)
+    chain = -(-units // grid) * -(-heads // 4) + 2 + 8 + 1 + 32
+    _, dw, _ = rope.norm_rope_bwd(_np(dy), _np(x), _np(w), pos, f, 1e-6, inter)
+    _, n, _ = rope.norm(_np(x), _np(w), 1e-6)
+    tol = chain * EPS32 * (1 + 2.0 ** -10) * (_partner_abs(_np(dy), 2 * len(f), inter) * np.abs(n)).sum((0, 1))
+    assert (np.abs(_np(got) - dw) <= tol + 1e-38).all(), (np.abs(_np(got) - dw) / tol).max()
+
+
+@pytest.mark.parametrize("inter", [False, True])
+def test_weight_gradient_of_every_unit(inter, cuda_device):
+    """A batch whose persistent CTAs take several units of frames each: dw
+    under the bound of the kernel's chain, far below one frame's share; and with
+    a gradient in one unit alone (of every round of the CTAs, and the last one,
+    of one frame) dw is that unit's."""
+    nle = _nle()
+    lengths = [4001, 1, 2999, 3500, 17]
+    x = _draw(lengths, 2, 1, 5)
+    d = _dev(x, cuda_device)
+    f = _freq(64)
+    ft = torch.from_numpy(f).to(cuda_device)
+    pos = rope.positions(x["cu"])
+    starts = [(int(a) + s, min(8, int(b - a) - s)) for a, b in zip(x["cu"][:-1], x["cu"][1:]) for s in range(0, b - a, 8)]
+    run = lambda dq, dk: nle.qk_norm_rope_bwd(dq, dk, d["cu"], ft, d["q"], d["k"], d["wq"], d["wk"],   # noqa: E731
+                                              interleaved=inter)
+    _, _, gwq, gwk = run(d["dq"], d["dk"])
+    _check_dw(gwq, x["dq"], x["q"], x["wq"], pos, f, len(starts), x["t"], 2, inter, cuda_device)
+    _check_dw(gwk, x["dk"], x["k"], x["wk"], pos, f, len(starts), x["t"], 1, inter, cuda_device)
+    grid = 2 * torch.cuda.get_device_properties(cuda_device).multi_processor_count
+    assert len(starts) > 2 * grid
+    for u in [0, *range(7, len(starts), grid), 500, 501, len(starts) - 1]:
+        a, n = starts[u]
+        rows = slice(a, a + n)
+        only = [torch.zeros_like(d[m]) for m in ("dq", "dk")]
+        for o, m in zip(only, ("dq", "dk")):
+            o[rows] = d[m][rows]
+        gq, gk, gwq, gwk = run(*only)
+        for g, gw, m, heads in ((gq, gwq, "q", 2), (gk, gwk, "k", 1)):
+            _check_dw(gw, x["d" + m][rows], x[m][rows], x["w" + m], pos[rows], f, 1, 8, heads, inter, cuda_device)
+            assert (gw != 0).all() and (g[rows] != 0).any()
+            g[rows] = 0
+            assert (g == 0).all()
