@@ -595,6 +595,9 @@ int launch_block_attn(const void *q, const void *k, const void *v, void *out, fl
     if (stride % 8 != 0 || !nle::aligned16(q) || !nle::aligned16(k) || !nle::aligned16(v) ||
         !nle::aligned16(out) || !nle::aligned4(lse) || (lse && !nle::aligned4(dev_status)))
         return NLE_ERR_MISALIGNED;
+    if (lse && (nle::begins_at(out, {q, k, v, cu_seqlens, dev_status}) ||
+                nle::begins_at(lse, {q, k, v, out, cu_seqlens, dev_status})))
+        return NLE_ERR_INVALID_ARG;
 
     nle::DeviceInfo di;
     int dev = 0;

@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cstdint>
+#include <initializer_list>
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -38,5 +39,13 @@ bool allow_max_dynamic_smem(const void *fn, int device, int smem_optin);
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+// Does p begin where one of the others does?
+inline bool begins_at(const void *p, std::initializer_list<const void *> others)
+{
+    for (const void *o : others)
+        if (o == p)
+            return true;
+    return false;
+}
 
 } // namespace nle

@@ -237,6 +237,7 @@ int nle_varlen_attn_fwd_ex(const void *q, const void *k, const void *v, void *ou
  *      lse[h][i] = ln sum_j exp(softmax_scale * q_i.k_j) over the frames j
  *      that frame i attends to (natural log); 4-byte aligned.  Entries of
  *      frames of no utterance are not written.
+ * An out or lse that begins where another buffer does is NLE_ERR_INVALID_ARG.
  *
  * nle_*_bwd: with P_ij = exp(s q_i.k_j - lse_i), s = softmax_scale, and
  * delta_i = sum_d dout_id out_id, all sums over the block (utterance):

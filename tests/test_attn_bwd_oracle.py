@@ -161,3 +161,22 @@ def test_status_off_its_alignment():
 def test_binding_names_missing_offsets():
     with pytest.raises(TypeError, match="cu_seqlens must be a CUDA tensor"):
         nle._n_seq(None, 0)
+
+
+@pytest.mark.parametrize("block", [200, None])
+def test_forward_outputs_that_begin_at_another_buffer(block):
+    """The forwards that keep the log-sum-exp: out and lse begin at no input and not at each other."""
+    names = ("q", "k", "v", "out", "lse", "cu_seqlens", "dev_status")
+
+    def f(**kw):
+        a = dict({n: 1024 * (i + 1) for i, n in enumerate(names)}, **kw)
+        head = [a[n] for n in names[:6]] + [1, 400, 8, 64]
+        tail = [0.0, 0, a["dev_status"], 0, 0, None]
+        if block:
+            return nle._lib.nle_block_attn_fwd_lse(*head, block, *tail)
+        return nle._lib.nle_varlen_attn_fwd_lse(*head, *tail)
+
+    for n in ("out", "lse"):
+        for i, m in enumerate(names):
+            if m != n:
+                assert f(**{n: 1024 * (i + 1)}) == nle.NLE_ERR_INVALID_ARG, (n, m)
