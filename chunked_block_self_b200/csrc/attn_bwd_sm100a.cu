@@ -19,8 +19,9 @@
 //   kind 1 (dQ): owner Q, dO (rows = queries), tiles K, V
 //     S = X x^T, D = Y y^T,  acc0 (dQ) += dS x
 // P is formed twice (once per kind): 7 products of 2*64 FLOP and 2 exps per
-// (query, key) pair instead of 5 and 1, which costs less than the fp32
-// atomics (32 KB per 128 x 128 pairs) that a single pass would add.
+// (query, key) pair instead of 5 and 1.  A single pass would have to sum dQ
+// across owners, in fp32 atomics or in partial sums added in order (32 KB per
+// 128 x 128 pairs, half of that with owners of 256 keys); it was not built.
 //
 // One persistent CTA per SM, 20 warps:
 //   warp 0   TMA producer: owner tiles (two stages), the segment's tiles into
@@ -32,20 +33,23 @@
 //   warps 4-19  elementwise, two streams of two warpgroups on alternate tiles:
 //            a lane owns one row of the tile (its TMEM lane), warpgroup g the
 //            columns 32 (g & 1) .. + 31.  P = exp2(S s log2e - lse log2e) and
-//            dS = P (D - delta) in fp32, each rounded once to bf16 (the A
-//            operands of the accumulating MMAs) and written over S.  lse and
-//            delta belong to the lane's row (kind 1), or to the columns
-//            (kind 0: fetched one tile ahead, +inf and 0 past the segment, so
-//            that P and dS vanish there).  At the end of an item the output
-//            rows: acc times s, rounded to bf16, the segment's rows only.
+//            dS = P (D - delta) in fp32, each rounded once to bf16 and written
+//            over S.  lse and delta belong to the lane's row (kind 1), or to the
+//            columns (kind 0: fetched one tile ahead, +inf and 0 past the
+//            segment, so that P and dS vanish there).  At the end of an item the
+//            output rows: acc times s, rounded to bf16, the segment's rows only.
 // TMEM (512 columns): stream p at 192 p: two S buffers of 64 (after use: P of
 // the group's columns in its first 16, dS in its last 16), D at + 128; acc0 at
 // 384, acc1 at 448.
 //
+// P and dS are rounded because the accumulating MMAs take 16-bit A operands at
+// the full rate; the forward rounds its P alike.  Against 64 bits each gradient
+// is then off by 0.0024 (relative, L2), 0.0017 of it the rounding of the result.
+//
 // What bounds it: the chain of a tile (S, read, exp, D, dS, write, accumulate)
 // takes about 2.4 k cycles, and two chains are in flight: about 1.2 k cycles a
 // tile, beside 512 for its 8192 exps and 512 (kind 1) or 640 (kind 0) for its
-// MMAs.  16 clips of 1950-4700 frames, 16 heads: 2.97 ms, 0.81 PFLOP/s over the
+// MMAs.  16 clips of 1950-4700 frames, 16 heads: 2.95 ms, 0.81 PFLOP/s over the
 // 7 products (0.49 of a measured bf16 GEMM), 0.58 over the formula's 5.  The
 // registers decide: 94 of the 96 that 640 threads leave, none spilled.  Beside
 // 200 KB of shared memory a spill lives in L2, and every form with more rows or
@@ -647,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // delta[h][f] = sum_d dO O (fp32): eight lanes per head row, four heads of a
 // frame per warp load.  Memory-bound: reads O and dO once.  Not unrolled: the
-// unrolled loop takes 38 registers instead of 29 and so runs fewer warps
+// unrolled loop takes 46 registers instead of 29 and runs 40 warps per SM, not 64
 // (41 -> 51 us on the batch of 128 utterances).
 __global__ void __launch_bounds__(256)
     attn_delta_kernel(const uint4 *out, const uint4 *dout, float *delta, int total, int heads)
@@ -736,11 +740,17 @@ int launch_attn_bwd(const nle_attn_bwd_args *a, int block, void *stream)
     float *delta = static_cast<float *>(a->workspace);
     const unsigned long long wait_ns = a->wait_limit_ns > 0 ? (unsigned long long)a->wait_limit_ns : 1000000000ull;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    // Blocks of more than one key tile, and at least one (block, head) per SM:
-    // whole blocks on chip (batch of 128 utterances: 395 us against 491 us here,
-    // with delta's 41 us in both).  One key tile leaves that kernel's second half
-    // idle (128-frame blocks: 372 against 344 us), and fewer items leave SMs
-    // idle (64 items: 17.1 against 14.0 us; 128: 19.0 against 21.0 us).
+    // Blocks longer than one key tile, and a (block, head) for every SM by the
+    // bound `units`: whole blocks on chip.  Whole blocks against tiles, us, with
+    // delta's 41 in both: batch of 128 utterances, blocks of 97: 461, 410; 128:
+    // 375, 352 (one key tile leaves the second half of that kernel idle); 129:
+    // 543, 606; 160: 467, 518; 200: 404, 502; 256: 393, 459.  Few items of 200
+    // frames, L2 flushed: 64: 24.6, 20.5; 96: 24.6, 24.6; 128: 26.6, 28.7; 160
+    // (a second round for twelve SMs): 36.8, 32.8; 256: 38.9, 41.0.  The bound
+    // counts an utterance of exactly one block twice, so 74 such items already
+    // pass for 148; and it is block_frames that is looked at, not the utterances:
+    // 512 of 100-128 frames take whole blocks too (377 against 363; of 40-80
+    // frames 360 against 272).
     const bool whole = block && !(a->flags & NLE_FLAG_SPLIT_ITEMS) &&
                        ((a->flags & NLE_FLAG_WHOLE_ITEMS) || (block > kRows && units * a->heads >= di.sm_count));
     if (whole) {

@@ -13,7 +13,8 @@
 //     dK_c += dS Q_u     A = dS in shared memory, K-major, B = Q rows
 //     dQ_x += dS^T K_c   A = the same shared memory read M-major: 128 queries
 //                        (two units), K = the tile's keys, B = K rows
-// dS is written once, as 64-query chunks of 128-byte rows (one key each),
+// P and dS are rounded once to bf16, the type that the MMAs take at the full
+// rate (errors as in attn_bwd_sm100a.cu).  dS is written once, as 64-query chunks of 128-byte rows (one key each),
 // 128-byte swizzled: a row-major operand for dK and a column-major one for dQ.
 //
 // One persistent CTA per SM, 16 warps:

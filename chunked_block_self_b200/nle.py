@@ -8,9 +8,13 @@ ImportError if it is missing -- there is no fallback path.  Build it with
 Functions named ``nle_*`` mirror the C entry points one to one; they take
 torch CUDA tensors (or, for the host table functions, numpy arrays) and the
 stream defaults to torch's current stream.  A non-zero status raises
-:class:`NLEError`.  The few helpers without the prefix (``block_attn``,
-``window_xattn``, ``window_query_rows``) only allocate outputs with torch
-and call the entry points.
+:class:`NLEError`.  The helpers without the prefix (``block_attn``,
+``window_xattn``, ``window_query_rows``, the training forms ``*_lse`` and
+``*_bwd`` ...) only allocate outputs with torch and call the entry points.
+
+Nothing here records gradients: tensors that require them are taken as they
+are, and results are detached.  The ``*_bwd`` functions are the gradients; a
+program calls them itself, or from a ``torch.autograd.Function`` of its own.
 """
 from __future__ import annotations
 
@@ -547,7 +551,8 @@ def block_attn_lse(q, k, v, cu_seqlens, block_frames: int = 200, softmax_scale: 
                    dev_status=None, flags: int = 0, wait_limit_ns: int = 0, stream=None):
     """(out, lse) of block attention: the output of :func:`block_attn` and what
     :func:`block_attn_bwd` needs of it, lse float32 [heads, frames].  q, k and
-    v may be views of one projection buffer (a common frame stride)."""
+    v have one shape and one frame stride: dense, or views of one projection
+    buffer.  Beside dense q and k (of :func:`qk_norm_rope`) v must be dense."""
     return _attn_lse(q, k, v, cu_seqlens, block_frames, softmax_scale, out, dev_status, flags, wait_limit_ns, stream)
 
 

@@ -249,7 +249,7 @@ int nle_varlen_attn_fwd_ex(const void *q, const void *k, const void *v, void *ou
  *
  * nle_attn_bwd_args (host struct, device pointers):
  *   q, k, v      bf16, as the forward's, frames row_stride_qkv elements
- *                apart (0: heads * 64; a multiple of 8)
+ *                apart (0: heads * 64; a multiple of 8), the same in all three
  *   out, dout    bf16 [total_frames][heads][64], dense: the forward's output
  *                and its gradient
  *   lse          float [heads][total_frames], of the forward
@@ -263,8 +263,8 @@ int nle_varlen_attn_fwd_ex(const void *q, const void *k, const void *v, void *ou
  *   flags        NLE_FLAG_*; NLE_FLAG_WHOLE_ITEMS and NLE_FLAG_SPLIT_ITEMS
  *                force a block gradient's work split (whole blocks on chip,
  *                or 128-row tiles of either side; by default whole blocks
- *                when block_frames is above 128 and there is a (block, head)
- *                for every SM).  The two sum in different orders: each gives
+ *                when block_frames is above 128 and heads * (n_seq +
+ *                total_frames / block_frames) reaches the number of SMs).  The two sum in different orders: each gives
  *                the same bits on every call, not the bits of the other
  *   cu_seqlens, n_seq, total_frames, heads, d_head, softmax_scale,
  *   dev_status, wait_limit_ns: as the forward's _ex form
@@ -322,7 +322,7 @@ int nle_varlen_attn_bwd(const nle_attn_bwd_args *args, void *stream);
  *   q_heads, k_heads  either may be 0 (that tensor's pointers are ignored)
  *   d_head       must be 64
  *   q_weight, k_weight  bf16 [64], 16-byte aligned; both NULL: no norm
- *   eps          >= 0
+ *   eps          >= 0 (with 0 a row of zeros gives NaN, as 0 / 0 does)
  *   inv_freq     double [rot_dim / 2], 8-byte aligned (may be NULL when
  *                rot_dim is 0)
  *   rot_dim      0, 16, 32, 48 or 64
@@ -339,12 +339,12 @@ int nle_varlen_attn_bwd(const nle_attn_bwd_args *args, void *stream);
  * nle_qk_norm_rope_bwd: from the gradients dq_out, dk_out of the outputs and
  * (read only with weights; may be NULL without) the inputs q, k: dq, dk, and
  * the weights' gradients dq_weight, dk_weight: nullable float [64], 4-byte
- * aligned, written, not accumulated.  dq may be dq_out or q, and dk dk_out or k (same pointer and
- * stride); other overlaps of dq, dk, the weights' gradients and the workspace
- * are not allowed, as in the forward.  workspace: with weights,
- * NLE_ROPE_BWD_WORKSPACE_BYTES of device scratch, 16-byte aligned, used by
- * this call alone until it has run; its content need not be kept.  Results
- * are the same bits on every call.
+ * aligned, written, not accumulated.  dq may be dq_out or q, and dk dk_out or
+ * k (same pointer and stride); other overlaps of dq, dk, the weights' gradients
+ * and the workspace are not allowed, as in the forward.  workspace: with
+ * weights, NLE_ROPE_BWD_WORKSPACE_BYTES of device scratch, 16-byte aligned,
+ * used by this call alone until it has run; its content need not be kept.
+ * Results are the same bits on every call.
  * One kernel on `stream` (two for the weights' gradients); no allocation.
  * Errors as for the attention entry points, before any launch.
  */
